@@ -7,8 +7,8 @@ library raises ImportError; there is no CPU fallback.
 
 Names follow the C ABI: ``Plan`` (rot_plan_create / rot_plan_destroy), ``rot_apply``,
 ``rot_quant``, ``rot_dequant``, ``w4a4_linear``, ``w4a4_group_partials``, ``w4a8_linear``,
-``w4a8_group_partials``,
-``harp_givens_blocks``, ``harp_qr_block``, ``check_device``.
+``w4a8_group_partials``, ``KV4Cache`` with ``kv4_append``, ``kv4_read``, ``kv4_attention`` and
+``kv4_slot``, ``harp_givens_blocks``, ``harp_qr_block``, ``check_device``.
 """
 from __future__ import annotations
 
@@ -54,6 +54,25 @@ _lib.rot_harp_cayley_block.argtypes = [C.POINTER(C.c_double), _int, C.POINTER(C.
 _lib.rot_plan_create_q8.argtypes = [C.POINTER(_vp), _int, _int, C.POINTER(_int), C.POINTER(C.POINTER(C.c_int8)),
                                     C.POINTER(C.c_float), C.POINTER(_i64), C.POINTER(C.POINTER(C.c_float)),
                                     C.POINTER(C.POINTER(_i32)), C.POINTER(C.c_int8)]
+
+
+class _KV4CacheStruct(C.Structure):
+    _fields_ = [("data", _vp), ("page_stride", _i64), ("pages", _i64), ("page", _int), ("heads", _int),
+                ("D", _int), ("G", _int), ("k_plan", _vp), ("v_plan", _vp)]
+
+
+class _KV4SeqsStruct(C.Structure):
+    _fields_ = [("table", _vp), ("table_stride", _i64), ("table_pages", _int), ("lens", _vp), ("cu", _vp),
+                ("B", _int), ("T", _i64)]
+
+
+_kvc, _kvs = C.POINTER(_KV4CacheStruct), C.POINTER(_KV4SeqsStruct)
+_lib.kv4_append.argtypes = [_kvc, _kvs, _vp, _i64, _i64, _vp, _i64, _i64, _int, _vp]
+_lib.kv4_read.argtypes = [_kvc, _kvs, _int, _vp, _vp, _int, _vp]
+_lib.kv4_attention_workspace.argtypes = [_kvc, _int, _i64, _int, _int, _i64, _i64, C.POINTER(C.c_size_t)]
+_lib.kv4_attention.argtypes = [_kvc, _kvs, _vp, _int, _i64, _i64, _int, C.c_float, _int, _int, _i64, _i64, _vp, _vp,
+                               C.c_size_t, _vp]
+_lib.kv4_slot.argtypes = [_kvc, _kvs, _i64, _int, C.POINTER(_i64)]
 _lib.rot_check_device.argtypes = []
 _lib.rot_test_inject.argtypes = [_int, _i64]
 _lib.rot_last_error.restype = C.c_char_p
@@ -62,7 +81,8 @@ for _f in ("rot_plan_create", "rot_plan_destroy", "rot_plan_info", "rot_apply", 
            "w4a4_linear", "w4a4_linear_noalloc", "w4a4_group_partials", "w4a8_linear", "w4a8_group_partials",
            "w4a4_linear_rot", "w4a4_linear_act_workspace", "w4a4_linear_act",
            "w4a4_tile_plan", "rot_harp_givens_blocks",
-           "rot_harp_qr_block", "rot_check_device", "rot_test_inject", "rot_harp_cayley_block", "rot_plan_create_q8"):
+           "rot_harp_qr_block", "rot_check_device", "rot_test_inject", "rot_harp_cayley_block", "rot_plan_create_q8",
+           "kv4_append", "kv4_read", "kv4_attention_workspace", "kv4_attention", "kv4_slot"):
     getattr(_lib, _f).restype = _int
 
 
@@ -458,6 +478,200 @@ def w4a4_tile_plan(M: int, N: int, K: int, G: int, sms: int, partials: bool = Fa
     _check(_lib.w4a4_tile_plan(M, N, K, G, sms, int(partials), out))
     keys = ("tiles_m", "tiles_n", "splits", "kb_per_split", "units", "grid")
     return {k: int(v) for k, v in zip(keys, out)}
+
+
+class KV4Cache:
+    """A paged key/value cache of one attention layer, held in 4 bits (rot_kv4_cache).
+
+    data: uint8 [pages, heads, page/32, 32 D + 128 D/G], any stride (a multiple of 16 bytes) from page to
+    page and dense within one, so that layers may share an allocation; its contents need no
+    initialisation. G: coordinates of a scale. k_plan / v_plan: the rotation (``Plan.rht(D, signs)``) that
+    keys / values are stored in, or None. Keeps references to data and plans.
+    """
+
+    def __init__(self, data, D: int, G: int, *, k_plan: "Plan | None" = None, v_plan: "Plan | None" = None):
+        import torch
+        D, G = int(D), int(G)
+        if not isinstance(data, torch.Tensor) or data.dtype != torch.uint8 or data.dim() != 4:
+            raise RotError(ROT_EINVAL, "data must be a 4-D uint8 tensor")
+        if D not in (64, 128, 256) or G not in (32, 64, 128, 256) or D % G:
+            raise RotError(ROT_EINVAL, f"D = {D} must be 64, 128 or 256, and G = {G} one of 32, 64, 128, 256 that divides D")
+        if data.shape[3] != self.tile_bytes(D, G):
+            raise RotError(ROT_EINVAL, f"data must have tiles of {self.tile_bytes(D, G)} bytes, got {data.shape[3]}")
+        if data.shape[1] < 1 or data.shape[2] < 1:
+            raise RotError(ROT_EINVAL, "data must hold at least one head and one tile to a page")
+        if data.numel() and not data[0].is_contiguous():
+            raise RotError(ROT_EINVAL, "data must be dense within a page")
+        for name, plan in (("k_plan", k_plan), ("v_plan", v_plan)):
+            if plan is not None and plan.K != D:
+                raise RotError(ROT_EINVAL, f"{name} must have K == D")
+        self.data, self.D, self.G = data, D, G
+        self.pages, self.heads, self.page = data.shape[0], data.shape[1], data.shape[2] * 32
+        self.k_plan, self.v_plan = k_plan, v_plan
+        dense = data.shape[1] * data.shape[2] * data.shape[3]
+        self._c = _KV4CacheStruct(data.data_ptr(), data.stride(0) if data.shape[0] > 1 else dense, self.pages,
+                                  self.page, self.heads, D, G, None, None)
+
+    @staticmethod
+    def tile_bytes(D: int, G: int) -> int:
+        """Bytes of 32 tokens of one head: keys, values and their scales."""
+        return 32 * D + 128 * D // G
+
+    @classmethod
+    def empty(cls, pages: int, page: int, heads: int, D: int, G: int, *, k_plan=None, v_plan=None, device="cuda"):
+        """An uninitialised cache of `pages` pages of `page` tokens (a multiple of 32)."""
+        import torch
+        if page <= 0 or page % 32:
+            raise RotError(ROT_EINVAL, f"page = {page} must be a positive multiple of 32")
+        data = torch.empty((pages, heads, page // 32, cls.tile_bytes(D, G)), dtype=torch.uint8, device=device)
+        return cls(data, D, G, k_plan=k_plan, v_plan=v_plan)
+
+    def _struct(self, current: int):
+        """The C view, checked against the current device and with the plans as they are now."""
+        if not self.data.is_cuda:
+            raise RotError(ROT_EINVAL, f"the cache must be on a CUDA device, not {self.data.device}")
+        _check_device(self.data.device.index, current, "the cache")
+        for name, plan in (("k_plan", self.k_plan), ("v_plan", self.v_plan)):
+            if plan is not None and not plan.handle.value:
+                raise RotError(ROT_EINVAL, f"the cache's {name} was closed")
+        self._c.k_plan = self.k_plan.handle if self.k_plan is not None else None
+        self._c.v_plan = self.v_plan.handle if self.v_plan is not None else None
+        return C.byref(self._c)
+
+
+def _kv4_seqs(table, lens, cu, T: int):
+    """Checked rot_kv4_seqs of page table, lengths and row offsets."""
+    import torch
+    pl = _arg(lens, "lens", dtype=torch.int32)
+    if lens.dim() != 1:
+        raise RotError(ROT_EINVAL, "lens must be 1-D")
+    B = lens.shape[0]
+    pt = _arg(table, "table", dtype=torch.int32, strided_rows=True)
+    if table.dim() != 2 or table.shape[0] != B:
+        raise RotError(ROT_EINVAL, f"table must be 2-D with one row for each of {B} sequences")
+    pc = None
+    if cu is not None:
+        pc = _arg(cu, "cu", dtype=torch.int32, shape=(B + 1,))
+    elif T != B:
+        raise RotError(ROT_EINVAL, f"without cu there is one new token per sequence: got {T} rows for {B} sequences")
+    cols = table.shape[1]
+    return C.byref(_KV4SeqsStruct(pt, max(table.stride(0), cols) if B > 1 else cols, cols, pl, pc, B, T))
+
+
+def _kv4_rows(t, name: str, heads, D: int):
+    """Checked address and strides of rows [T, heads, D] with unit stride along D."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise RotError(ROT_EINVAL, f"{name} must be a torch tensor on a CUDA device")
+    _check_device(t.device.index, torch.cuda.current_device(), name)
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise RotError(ROT_EINVAL, f"{name} must be bf16 or fp32, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+        raise RotError(ROT_EINVAL, f"{name} must have shape [T, {'Hq' if heads is None else heads}, {D}], got {tuple(t.shape)}")
+    if t.numel() and t.stride(2) != 1:
+        raise RotError(ROT_EINVAL, f"{name} must have unit stride along its last dimension")
+    # (the stride of a dimension of one element may be anything)
+    head = t.stride(1) if t.shape[1] > 1 else D
+    return C.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else head * t.shape[1], head
+
+
+def _kv4_empty(shape, dtype, device, stream):
+    """torch.empty for a launch on `stream`: the memory belongs to the stream that uses it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def kv4_append(cache: KV4Cache, k, v, table, lens, cu=None, *, stream=None) -> None:
+    """Rotate, quantise and write the new tokens' keys and values (bf16 or fp32 [T, heads, D], any token and
+    head strides) into the cache. table int32 [B, pages of a sequence], lens int32 [B] with the new tokens
+    among them, cu int32 [B + 1] the offsets of each sequence's rows (None: one new token each)."""
+    import torch
+    cs = cache._struct(torch.cuda.current_device())
+    pk, kt, kh = _kv4_rows(k, "k", cache.heads, cache.D)
+    pv, vt, vh = _kv4_rows(v, "v", cache.heads, cache.D)
+    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+        raise RotError(ROT_EINVAL, "k and v must have the same dtype and number of rows")
+    ss = _kv4_seqs(table, lens, cu, k.shape[0])
+    _check(_lib.kv4_append(cs, ss, pk, kt, kh, pv, vt, vh, _dtype_code(k), _stream(stream)))
+
+
+def kv4_read(cache: KV4Cache, table, lens, cu=None, *, total=None, inverse: bool = False, out_dtype=None, out=None,
+             stream=None):
+    """The new tokens' keys and values as the cache holds them (cu may name whole sequences): (k, v) of
+    [total, heads, D], total the packed rows (default: one for each sequence). Stored basis, or with
+    inverse the original one; bf16 (default) or fp32. Rows behind the last sequence are left as they were."""
+    import torch
+    cs = cache._struct(torch.cuda.current_device())
+    T = int(total) if total is not None else lens.shape[0]
+    shape = (T, cache.heads, cache.D)
+    if out is None:
+        kind = out_dtype or torch.bfloat16
+        out = tuple(_kv4_empty(shape, kind, cache.data.device, stream) for _ in range(2))
+    k, v = out
+    pk = _arg(k, "out[0]", dtype=(torch.float32, torch.bfloat16), shape=shape)
+    pv = _arg(v, "out[1]", dtype=k.dtype, shape=shape)
+    ss = _kv4_seqs(table, lens, cu, T)
+    _check(_lib.kv4_read(cs, ss, int(inverse), pk, pv, _dtype_code(k), _stream(stream)))
+    return k, v
+
+
+def _kv4_sizes(cache, table, max_new, max_len, cu, T: int):
+    """The sizes that a launch is laid out for, where the caller names none."""
+    if max_new is None:
+        max_new = 1 if cu is None else T
+    if max_len is None:
+        max_len = table.shape[1] * cache.page
+    return int(max_new), int(max_len)
+
+
+def kv4_attention_workspace(cache: KV4Cache, B: int, T: int, Hq: int, *, max_new: int, max_len: int,
+                            window: int = 0) -> int:
+    """Bytes of the workspace that kv4_attention needs for these sizes (0: none)."""
+    n = C.c_size_t()
+    _check(_lib.kv4_attention_workspace(C.byref(cache._c), B, T, Hq, window, max_new, max_len, C.byref(n)))
+    return int(n.value)
+
+
+def kv4_attention(q, cache: KV4Cache, table, lens, cu=None, *, max_new=None, max_len=None, scale=None,
+                  causal: bool = True, window: int = 0, out=None, workspace=None, stream=None):
+    """softmax(scale q k) v of the new tokens' queries (bf16 or fp32 [T, Hq, D]) over the cache, which holds
+    their own keys and values already; bf16 [T, Hq, D]. table, lens and cu as for kv4_append; scale 1/sqrt(D)
+    unless given; causal by position, with the last `window` tokens only if window > 0. max_new and max_len
+    (the most new tokens and the longest length of a sequence) size the launch: give them where they are
+    known, since they cannot be read off device tensors. workspace: uint8, allocated here if not given."""
+    import torch
+    cs = cache._struct(torch.cuda.current_device())
+    pq, qt, qh = _kv4_rows(q, "q", None, cache.D)
+    T, Hq = q.shape[0], q.shape[1]
+    ss = _kv4_seqs(table, lens, cu, T)
+    max_new, max_len = _kv4_sizes(cache, table, max_new, max_len, cu, T)
+    n = C.c_size_t()
+    _check(_lib.kv4_attention_workspace(cs, lens.shape[0], T, Hq, window, max_new, max_len, C.byref(n)))
+    if out is None:
+        out = _kv4_empty((T, Hq, cache.D), torch.bfloat16, q.device, stream)
+    po = _arg(out, "out", dtype=torch.bfloat16, shape=(T, Hq, cache.D))
+    if workspace is None and n.value:
+        workspace = _kv4_empty((n.value,), torch.uint8, q.device, stream)
+    pw, nw = (_arg(workspace, "workspace", dtype=torch.uint8), workspace.numel()) if workspace is not None else (None, 0)
+    _check(_lib.kv4_attention(cs, ss, pq, _dtype_code(q), qt, qh, Hq, cache.D ** -0.5 if scale is None else scale,
+                              int(causal), window, max_new, max_len, po, pw, nw, _stream(stream)))
+    return out
+
+
+def kv4_slot(cache: KV4Cache, table, lens, cu, row: int, head: int, *, total=None):
+    """Host: (sequence, position, byte offset of the tile) of packed row `row` of a key head, from numpy int32
+    table, lens and cu (or None): sequence -1 behind the last one, offset -1 where the row has no place."""
+    tb, ln = np.ascontiguousarray(table, dtype=np.int32), np.ascontiguousarray(lens, dtype=np.int32)
+    c = np.ascontiguousarray(cu, dtype=np.int32) if cu is not None else None
+    ss = _KV4SeqsStruct(tb.ctypes.data, tb.shape[1], tb.shape[1], ln.ctypes.data, c.ctypes.data if c is not None else None,
+                        ln.size, ln.size if total is None else int(total))
+    out = (_i64 * 3)()
+    _check(_lib.kv4_slot(C.byref(cache._c), C.byref(ss), int(row), int(head), out))
+    return tuple(int(x) for x in out)
 
 
 def harp_givens_blocks(theta) -> np.ndarray:

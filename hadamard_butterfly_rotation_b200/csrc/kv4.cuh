@@ -1,0 +1,160 @@
+// The paged 4-bit key/value cache: tile layout, addressing and the pieces that its kernels share.
+//
+// A page holds `page` tokens of every head as page/32 tiles per head; a tile is 32 tokens of one
+// head, keys and values, contiguous, so that one bulk copy brings all that the attention reads of it:
+//   keys          [32 t][4 c][D/32 j][8 i]              codes, coordinate 32 j + 8 c + i of token t
+//   values        [2 s][2 h][8 r][4 c][2 b][D/32 j][4 i]  token 16 s + 8 h + 2 c + b, coordinate 32 j + 4 r + i
+//   key scales    [32 t][NG]                            binary16
+//   value scales  [16 pairs][NG][2 b]                   binary16, token 2 pair + b
+// Within the tile the order is that of the m16n8k16 A fragments of lane 4 r + c: a lane reads its
+// codes of a token (keys) or of a token pair (values) as one contiguous piece, and the 32 lanes'
+// pieces follow one another, so the reads need no shuffles and meet no bank conflict.
+#pragma once
+
+#include "rot_internal.cuh"
+
+namespace rotb {
+
+constexpr int KV4_TILE = 32;  // tokens of a tile
+
+// What the kernels are given of a cache and of the sequences in it.
+struct Kv4View {
+  uint8_t* data;
+  int64_t page_stride;  // bytes from page to page
+  int64_t pages;
+  int64_t table_stride;
+  int64_t T;              // packed new rows
+  const int32_t* table;   // [B, table_pages]
+  const int32_t* lens;    // [B]
+  const int32_t* cu;      // [B + 1], or NULL: one new token per sequence
+  const uint32_t* k_sign;  // sign masks of the rotations (rot_plan_s::d_signmask), or NULL
+  const uint32_t* v_sign;
+  int table_pages;
+  int tpp;                // tiles of a page
+  int heads;
+  int B;
+  int tile_bytes;
+  int k_rot, v_rot;       // whether keys / values are stored rotated
+};
+
+__host__ __device__ constexpr int kv4_tile_bytes(int D, int NG) { return 32 * D + 128 * NG; }
+
+// New tokens of sequence b: rows [*first, *first + n) of the packed rows, the first at position *pos (the
+// last before the sequence's end). Rows outside [0, T) never count.
+__host__ __device__ inline int kv4_new_rows(const Kv4View& c, int b, int64_t* first, int64_t* pos) {
+  const int64_t end = c.cu ? c.cu[b + 1] : (int64_t)b + 1;
+  const int64_t lo = c.cu ? (c.cu[b] > 0 ? c.cu[b] : 0) : b, hi = end < c.T ? end : c.T;
+  *first = lo;
+  *pos = (int64_t)c.lens[b] - (end - lo);
+  return hi > lo ? (int)(hi - lo) : 0;
+}
+
+// Sequence of packed row t: the last b with cu[b] <= t, or -1 behind the last sequence.
+__host__ __device__ inline int kv4_seq_of(const Kv4View& c, int64_t t) {
+  if (!c.cu) return t < c.B ? (int)t : -1;
+  int lo = 0, hi = c.B;  // invariant: cu[lo] <= t < cu[hi] once both ends hold
+  if (t < c.cu[0] || t >= c.cu[c.B]) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (c.cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Byte offset of head h's tile `tile` (token >> 5) of sequence b, or -1 where the table has no such
+// page or names one outside the cache: nothing is read or written there.
+__host__ __device__ inline int64_t kv4_tile_at(const Kv4View& c, int b, int64_t tile, int h) {
+  const int64_t slot = tile / c.tpp;
+  if (tile < 0 || slot >= c.table_pages) return -1;
+  const int64_t page = c.table[(int64_t)b * c.table_stride + slot];
+  if (page < 0 || page >= c.pages) return -1;
+  return page * c.page_stride + ((int64_t)h * c.tpp + (tile - slot * c.tpp)) * c.tile_bytes;
+}
+
+// Where packed row `row` of head h lies: its sequence (-1 behind the last one), its position and its
+// tile's byte offset (-1: a position below zero, or a page outside the cache).
+struct Kv4Slot {
+  int seq;
+  int64_t pos, at;
+};
+__host__ __device__ inline Kv4Slot kv4_slot_of(const Kv4View& c, int64_t row, int h) {
+  Kv4Slot p{-1, -1, -1};
+  if (row >= c.T) return p;
+  p.seq = kv4_seq_of(c, row);
+  if (p.seq < 0) return p;
+  const int64_t behind = c.cu ? (int64_t)c.cu[p.seq + 1] - row : 1;  // rows from this one to its sequence's end
+  p.pos = (int64_t)c.lens[p.seq] - behind;
+  if (p.pos >= 0) p.at = kv4_tile_at(c, p.seq, p.pos >> 5, h);
+  return p;
+}
+
+#ifdef __CUDACC__
+// +-v by bit `bit` of a sign mask word
+__device__ __forceinline__ float kv4_signed(float v, uint32_t word, int hi) {
+  return __uint_as_float(__float_as_uint(v) ^ ((hi ? word : word << 16) & 0x80000000u));
+}
+
+// Unnormalised Walsh-Hadamard transform of rows spread over `LANES` neighbouring lanes, V coordinates
+// each: the lowest log2 V stages in registers, the others by shuffles.
+template <int V, int LANES>
+__device__ __forceinline__ void kv4_fwht(float (&v)[V], int lane) {
+#pragma unroll
+  for (int s = 1; s < V; s *= 2)
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!(i & s)) {
+        const float a = v[i], b = v[i + s];
+        v[i] = a + b;
+        v[i + s] = a - b;
+      }
+#pragma unroll
+  for (int m = 1; m < LANES; m *= 2) {
+    const float sg = (lane & m) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = fmaf(v[i], sg, __shfl_xor_sync(0xffffffffu, v[i], m));
+  }
+}
+
+__device__ __forceinline__ float kv4_max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t kv4_pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+#endif
+
+// launchers: arguments already checked (kv4_api.cu)
+struct Kv4Rows {  // strides in elements
+  const void* k;
+  const void* v;
+  int64_t k_token, k_head, v_token, v_head;
+  int dtype;
+};
+rot_status kv4_append_launch(const Kv4View& c, int D, int NG, const Kv4Rows& in, cudaStream_t s);
+rot_status kv4_read_launch(const Kv4View& c, int D, int NG, const Kv4Rows& out, bool inverse, cudaStream_t s);
+struct Kv4Query {
+  const void* q;
+  int64_t q_token, q_head;  // elements
+  int q_dtype;
+  void* out;                // bf16 [T, Hq, D]
+  int Hq;
+  int causal, window;
+  float scale;
+  float* partial;           // [T * Hq, splits, D] then [T * Hq, splits, 2], NULL when splits == 1
+};
+struct Kv4Split {
+  int rows;      // query rows of a CTA (8 per n-tile)
+  int chunks;    // row chunks of a sequence and key head
+  int splits;    // parts of the length
+};
+Kv4Split kv4_split(int D, int B, int heads, int share, int window, int64_t max_new, int64_t max_len, int sms);
+rot_status kv4_attention_launch(const Kv4View& c, int D, int NG, const Kv4Query& q, const Kv4Split& sp,
+                                cudaStream_t s);
+
+}  // namespace rotb

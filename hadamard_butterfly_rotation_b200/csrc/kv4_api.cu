@@ -1,0 +1,175 @@
+// C-ABI entry points of the 4-bit key/value cache: argument checks and dispatch.
+#include <cmath>
+#include <cstdint>
+
+#include "kv4.cuh"
+
+using namespace rotb;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+rot_status check_rotation(rot_plan_t plan, int D, const char* fn, const char* which) {
+  if (!plan) return ROT_OK;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev != plan->device) return set_error(ROT_EINVAL, std::string(fn) + ": " + which + " belongs to another device");
+  if (plan->K != D) return set_error(ROT_EINVAL, std::string(fn) + ": " + which + " must have K == D");
+  if (plan->chunk_log2 < 0 || (1 << plan->chunk_log2) != D)
+    return set_error(ROT_EUNSUPPORTED, std::string(fn) + ": " + which + " must be one signed Walsh-Hadamard transform of size D");
+  return ROT_OK;
+}
+
+// Shape of the cache; `device` also checks what the device calls need
+rot_status check_cache(const rot_kv4_cache* c, const char* fn, bool device) {
+  if (!c) return set_error(ROT_EINVAL, std::string(fn) + ": cache is NULL");
+  if (c->D != 64 && c->D != 128 && c->D != 256) return set_error(ROT_EINVAL, std::string(fn) + ": D must be 64, 128 or 256");
+  if (c->G != 32 && c->G != 64 && c->G != 128 && c->G != 256)
+    return set_error(ROT_EINVAL, std::string(fn) + ": G must be 32, 64, 128 or 256");
+  if (c->D % c->G != 0) return set_error(ROT_EINVAL, std::string(fn) + ": G must divide D");
+  if (c->page <= 0 || c->page % KV4_TILE != 0)
+    return set_error(ROT_EINVAL, std::string(fn) + ": page must be a positive multiple of 32");
+  if (c->heads <= 0 || c->pages < 0) return set_error(ROT_EINVAL, std::string(fn) + ": need heads > 0, pages >= 0");
+  const int64_t bytes = (int64_t)c->heads * (c->page / KV4_TILE) * kv4_tile_bytes(c->D, c->D / c->G);
+  if (c->page_stride < bytes || c->page_stride % 16 != 0)
+    return set_error(ROT_EINVAL, std::string(fn) + ": page_stride must be a multiple of 16 and hold a page");
+  if (!device) return ROT_OK;
+  if (c->pages > 0 && (!c->data || !aligned16(c->data)))
+    return set_error(ROT_EINVAL, std::string(fn) + ": data must be non-NULL and 16-byte aligned");
+  rot_status st = check_rotation(c->k_plan, c->D, fn, "k_plan");
+  return st ? st : check_rotation(c->v_plan, c->D, fn, "v_plan");
+}
+
+rot_status check_seqs(const rot_kv4_seqs* s, const char* fn) {
+  if (!s) return set_error(ROT_EINVAL, std::string(fn) + ": seqs is NULL");
+  if (s->B < 0 || s->T < 0 || s->table_pages < 0 || s->table_stride < s->table_pages)
+    return set_error(ROT_EINVAL, std::string(fn) + ": need B >= 0, T >= 0, 0 <= table_pages <= table_stride");
+  if (!s->cu && s->T != s->B) return set_error(ROT_EINVAL, std::string(fn) + ": without cu there is one row per sequence");
+  if (s->T > 0x7fffffff) return set_error(ROT_EUNSUPPORTED, std::string(fn) + ": at most 2^31 - 1 rows");
+  if (s->B > 0 && (!s->lens || (s->table_pages > 0 && !s->table)))
+    return set_error(ROT_EINVAL, std::string(fn) + ": table and lens must be non-NULL");
+  return ROT_OK;
+}
+
+Kv4View view(const rot_kv4_cache* c, const rot_kv4_seqs* s) {
+  Kv4View v{};
+  v.data = static_cast<uint8_t*>(c->data);
+  v.page_stride = c->page_stride;
+  v.pages = c->pages;
+  v.tpp = c->page / KV4_TILE;
+  v.heads = c->heads;
+  v.tile_bytes = kv4_tile_bytes(c->D, c->D / c->G);
+  v.k_rot = c->k_plan != nullptr;
+  v.v_rot = c->v_plan != nullptr;
+  v.k_sign = c->k_plan && c->k_plan->has_signs ? c->k_plan->d_signmask : nullptr;
+  v.v_sign = c->v_plan && c->v_plan->has_signs ? c->v_plan->d_signmask : nullptr;
+  v.table = s->table;
+  v.table_stride = s->table_stride;
+  v.table_pages = s->table_pages;
+  v.lens = s->lens;
+  v.cu = s->cu;
+  v.B = s->B;
+  v.T = s->T;
+  return v;
+}
+
+rot_status check_rows(const void* p, int64_t token, int64_t head, int heads, int D, int dtype, const char* what) {
+  const int es = dtype == ROT_BF16 ? 2 : 4;
+  if (!p || !aligned16(p)) return set_error(ROT_EINVAL, std::string(what) + " must be non-NULL and 16-byte aligned");
+  if (token < 0 || head < D || (token * es) % 16 != 0 || (head * es) % 16 != 0)
+    return set_error(ROT_EINVAL, std::string(what) + ": strides must be multiples of 16 bytes, heads at least D apart");
+  return ROT_OK;
+}
+
+bool bad_dtype(int t) { return t != ROT_F32 && t != ROT_BF16; }
+
+rot_status check_attention(const rot_kv4_cache* c, int Hq, int window, int64_t max_new, int64_t max_len, const char* fn) {
+  if (Hq <= 0 || Hq % c->heads != 0)
+    return set_error(ROT_EINVAL, std::string(fn) + ": Hq must be a positive multiple of the cache's heads");
+  if (window < 0 || max_new < 0 || max_len < 0)
+    return set_error(ROT_EINVAL, std::string(fn) + ": need window >= 0, max_new >= 0, max_len >= 0");
+  return ROT_OK;
+}
+
+int64_t attention_floats(const Kv4Split& sp, int64_t T, int Hq, int D) {
+  return sp.splits > 1 ? T * Hq * sp.splits * (D + 2) : 0;
+}
+
+}  // namespace
+
+extern "C" rot_status kv4_append(const rot_kv4_cache* cache, const rot_kv4_seqs* seqs, const void* K,
+                                 int64_t k_token, int64_t k_head, const void* V, int64_t v_token,
+                                 int64_t v_head, int dtype, void* stream) {
+  rot_status st = check_cache(cache, "kv4_append", true);
+  if (st || (st = check_seqs(seqs, "kv4_append"))) return st;
+  if (bad_dtype(dtype)) return set_error(ROT_EINVAL, "kv4_append: dtype must be ROT_F32 or ROT_BF16");
+  if (seqs->T == 0 || seqs->B == 0) return ROT_OK;
+  if ((st = check_rows(K, k_token, k_head, cache->heads, cache->D, dtype, "kv4_append: K"))) return st;
+  if ((st = check_rows(V, v_token, v_head, cache->heads, cache->D, dtype, "kv4_append: V"))) return st;
+  return kv4_append_launch(view(cache, seqs), cache->D, cache->D / cache->G,
+                           Kv4Rows{K, V, k_token, k_head, v_token, v_head, dtype}, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" rot_status kv4_read(const rot_kv4_cache* cache, const rot_kv4_seqs* seqs, int inverse, void* K,
+                               void* V, int dtype, void* stream) {
+  rot_status st = check_cache(cache, "kv4_read", true);
+  if (st || (st = check_seqs(seqs, "kv4_read"))) return st;
+  if (bad_dtype(dtype)) return set_error(ROT_EINVAL, "kv4_read: dtype must be ROT_F32 or ROT_BF16");
+  if (seqs->T == 0 || seqs->B == 0) return ROT_OK;
+  if (!K || !V || !aligned16(K) || !aligned16(V))
+    return set_error(ROT_EINVAL, "kv4_read: K and V must be non-NULL and 16-byte aligned");
+  const int64_t head = cache->D, token = head * cache->heads;
+  return kv4_read_launch(view(cache, seqs), cache->D, cache->D / cache->G,
+                         Kv4Rows{K, V, token, head, token, head, dtype}, inverse != 0, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" rot_status kv4_attention_workspace(const rot_kv4_cache* cache, int B, int64_t T, int Hq, int window,
+                                              int64_t max_new, int64_t max_len, size_t* bytes) {
+  rot_status st = check_cache(cache, "kv4_attention_workspace", false);
+  if (st || (st = check_attention(cache, Hq, window, max_new, max_len, "kv4_attention_workspace"))) return st;
+  if (!bytes || B < 0 || T < 0) return set_error(ROT_EINVAL, "kv4_attention_workspace: need bytes, B >= 0, T >= 0");
+  const Kv4Split sp = kv4_split(cache->D, B, cache->heads, Hq / cache->heads, window, max_new, max_len, sm_count());
+  *bytes = (size_t)attention_floats(sp, T, Hq, cache->D) * 4;
+  return ROT_OK;
+}
+
+extern "C" rot_status kv4_attention(const rot_kv4_cache* cache, const rot_kv4_seqs* seqs, const void* Q,
+                                    int q_dtype, int64_t q_token, int64_t q_head, int Hq, float scale, int causal,
+                                    int window, int64_t max_new, int64_t max_len, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  rot_status st = check_cache(cache, "kv4_attention", true);
+  if (st || (st = check_seqs(seqs, "kv4_attention"))) return st;
+  if ((st = check_attention(cache, Hq, window, max_new, max_len, "kv4_attention"))) return st;
+  if (bad_dtype(q_dtype)) return set_error(ROT_EINVAL, "kv4_attention: q_dtype must be ROT_F32 or ROT_BF16");
+  if (window > 0 && !causal) return set_error(ROT_EINVAL, "kv4_attention: a window needs causal = 1");
+  if (!std::isfinite(scale)) return set_error(ROT_EINVAL, "kv4_attention: scale must be finite");
+  if (seqs->T == 0 || seqs->B == 0) return ROT_OK;
+  if ((st = check_rows(Q, q_token, q_head, Hq, cache->D, q_dtype, "kv4_attention: Q"))) return st;
+  if (!out || !aligned16(out)) return set_error(ROT_EINVAL, "kv4_attention: out must be non-NULL and 16-byte aligned");
+  const Kv4Split sp =
+      kv4_split(cache->D, seqs->B, cache->heads, Hq / cache->heads, window, max_new, max_len, sm_count());
+  const int64_t need = attention_floats(sp, seqs->T, Hq, cache->D) * 4;
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < (size_t)need))
+    return set_error(ROT_EINVAL, "kv4_attention: workspace must be 16-byte aligned and hold "
+                                 "kv4_attention_workspace bytes");
+  Kv4Query q{Q, q_token, q_head, q_dtype, out, Hq, causal != 0, window, scale,
+             need > 0 ? static_cast<float*>(workspace) : nullptr};
+  return kv4_attention_launch(view(cache, seqs), cache->D, cache->D / cache->G, q, sp,
+                              static_cast<cudaStream_t>(stream));
+}
+
+extern "C" rot_status kv4_slot(const rot_kv4_cache* cache, const rot_kv4_seqs* seqs, int64_t row, int head,
+                               int64_t* out) {
+  rot_status st = check_cache(cache, "kv4_slot", false);
+  if (st || (st = check_seqs(seqs, "kv4_slot"))) return st;
+  if (!out || row < 0 || row >= seqs->T || head < 0 || head >= cache->heads)
+    return set_error(ROT_EINVAL, "kv4_slot: need out, 0 <= row < T, 0 <= head < heads");
+  rot_kv4_cache shape = *cache;
+  shape.k_plan = shape.v_plan = nullptr;
+  const Kv4Slot p = kv4_slot_of(view(&shape, seqs), row, head);
+  out[0] = p.seq;
+  out[1] = p.pos;
+  out[2] = p.at;
+  return ROT_OK;
+}

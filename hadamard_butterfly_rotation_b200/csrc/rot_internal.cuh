@@ -98,6 +98,10 @@ struct W4A4TilePlan {
 rot_status w4a4_tile_plan_compute(int64_t M, int64_t N, int64_t K, int G, int sms, bool partials,
                                   W4A4TilePlan* out);
 
+// 4-bit key/value cache (kv4_cache.cu, kv4_attention.cu; their launchers are in kv4.cuh)
+rot_status kv4_cache_fetch_device_error();
+rot_status kv4_attention_fetch_device_error();
+
 // ---------------------------------------------------------------- device helpers
 #ifdef __CUDACC__
 // (a, b) <- (a + b, a - b) on two register pairs with packed fp32x2 adds

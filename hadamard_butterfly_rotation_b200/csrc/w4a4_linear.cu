@@ -1696,5 +1696,9 @@ extern "C" rot_status rot_check_device(void) {
   if (e != cudaSuccess) return rotb::cuda_error(e, "rot_check_device");
   rot_status st = rotb::fwht_fetch_device_error();
   rot_status st2 = rotb::w4a4_fetch_device_error();
+  if (st == ROT_OK) st = st2;
+  st2 = rotb::kv4_cache_fetch_device_error();
+  if (st == ROT_OK) st = st2;
+  st2 = rotb::kv4_attention_fetch_device_error();
   return st != ROT_OK ? st : st2;
 }

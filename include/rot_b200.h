@@ -252,8 +252,93 @@ rot_status rot_plan_create_q8(rot_plan_t* out, int K, int n_stages, const int* r
                               const int8_t* const* codes, const float* scales, const int64_t* n_blocks,
                               const float* const* mixers, const int32_t* const* perms, const int8_t* signs);
 
-/* Synchronise the current device and report device-side errors recorded by bounded
- * waits (ROT_ETIMEOUT) since the last call; clears the record. */
+/* A key/value cache held in 4 bits, paged, of one attention layer.
+ *
+ * data holds `pages` pages, page_stride bytes apart (a multiple of 16, at least a page's bytes), each
+ * dense: [heads][page / 32 tiles][tile bytes], tile bytes = 32 D + 128 D / G. A tile is 32 consecutive
+ * tokens of one key/value head: int4 codes (two's complement, -7..7, low nibble first, 32-bit
+ * little-endian words) in groups of G coordinates with one binary16 scale each, value = code * scale,
+ * quantised as by rot_quant, in the order that the attention reads (NG = D / G):
+ *   keys          [32 t][4 c][D/32 j][8 i]                 coordinate 32 j + 8 c + i of token t
+ *   values        [2 s][2 h][8 r][4 c][2 b][D/32 j][4 i]   token 16 s + 8 h + 2 c + b, coordinate 32 j + 4 r + i
+ *   key scales    [32 t][NG]
+ *   value scales  [16 u][NG][2 b]                          token 2 u + b
+ * D is 64, 128 or 256, G is 32, 64, 128 or 256 and divides D, page is a positive multiple of 32.
+ * k_plan / v_plan: NULL, or the rotation that keys / values are stored in: a plan with K = D that is one
+ * signed Walsh-Hadamard transform (rot_plan_info chunk == D); other plans give ROT_EUNSUPPORTED. The
+ * softmax's products are the same in either basis, (T q).(T k) = q.k, and in the rotated one outliers
+ * spread over the group scales [HARP abstract; Hadamard-Int4-Accuracy wiki, Hypothesis]. */
+typedef struct {
+  void* data;
+  int64_t page_stride;
+  int64_t pages;
+  int page;
+  int heads;
+  int D;
+  int G;
+  rot_plan_t k_plan;
+  rot_plan_t v_plan;
+} rot_kv4_cache;
+
+/* The sequences that a call works on (device pointers).
+ *   table  int32 [B, table_pages], rows table_stride elements apart: the pages of each sequence, token x
+ *          of sequence b in page table[b][x / page]
+ *   lens   int32 [B]: tokens of each sequence, this call's new ones among them
+ *   cu     int32 [B + 1] ascending: sequence b's new tokens are the packed rows cu[b] .. cu[b+1] - 1, the
+ *          last ones of its lens[b] tokens; none, or all of them, may be new. NULL: one for each (T == B).
+ *   T      packed rows; rows from cu[B] on belong to no sequence, are not read and stay as they were
+ * A page that a call writes belongs to one sequence; where two name it, which one's rows it holds is not
+ * specified. A new token at a position below 0 (more new tokens than lens) has no place: it is not
+ * written, read as zeros, and its attention is zero. A position whose table entry is missing or names no
+ * page of the cache is skipped in the same way, is not attended to, and rot_check_device reports it
+ * (ROT_EINVAL). lens and cu are read on the device only, so a captured call serves changing lengths. */
+typedef struct {
+  const int32_t* table;
+  int64_t table_stride;
+  int table_pages;
+  const int32_t* lens;
+  const int32_t* cu;
+  int B;
+  int64_t T;
+} rot_kv4_seqs;
+
+/* Rotate, quantise and write the new tokens' keys and values: K, V of dtype [T, heads, D], rows
+ * *_token / *_head elements apart, 16-byte aligned. A group that holds a NaN, or whose scale overflows
+ * binary16, stores that scale and codes of 0 and reads back as NaN. Nothing else of the cache changes. */
+rot_status kv4_append(const rot_kv4_cache* cache, const rot_kv4_seqs* seqs, const void* K, int64_t k_token,
+                      int64_t k_head, const void* V, int64_t v_token, int64_t v_head, int dtype, void* stream);
+
+/* Read the new tokens' rows back (cu may name whole sequences): q * s as stored (inverse = 0) or in the
+ * original basis T^T (q * s) (inverse = 1), to dense K, V of dtype [T, heads, D]. */
+rot_status kv4_read(const rot_kv4_cache* cache, const rot_kv4_seqs* seqs, int inverse, void* K, void* V,
+                    int dtype, void* stream);
+
+/* Attention of the new tokens' queries over the cache:
+ *   out[t, h] = sum_x p_x v_x / sum_x p_x,  p_x = exp(scale q[t, h].k_x)
+ * over the tokens x of t's sequence that t sees: all of them (causal = 0), those up to its own position
+ * (causal = 1), or the last `window` of these (window > 0; 0 for no window). Query head h reads key head
+ * h / (Hq / heads). A row that sees nothing gives zeros. Q of q_dtype [T, Hq, D], rows q_token / q_head
+ * elements apart; out bf16 [T, Hq, D] dense (16-bit products, so no fp32 output is offered: the rotated
+ * query and the probabilities are rounded to binary16, about 2^-12 each).
+ *   max_new, max_len   what the launch is sized for: the most new tokens, and the longest length, of a
+ *                      sequence. Larger ones are still computed in full, only less evenly spread.
+ *   workspace          16-byte aligned, kv4_attention_workspace bytes for the same arguments (NULL where
+ *                      that is 0); it holds the parts of a split length during the call and needs no
+ *                      initialisation. Calls that may overlap on the GPU need one each. */
+rot_status kv4_attention_workspace(const rot_kv4_cache* cache, int B, int64_t T, int Hq, int window,
+                                   int64_t max_new, int64_t max_len, size_t* bytes);
+rot_status kv4_attention(const rot_kv4_cache* cache, const rot_kv4_seqs* seqs, const void* Q, int q_dtype,
+                         int64_t q_token, int64_t q_head, int Hq, float scale, int causal, int window,
+                         int64_t max_new, int64_t max_len, void* out, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Host only: where the kernels find packed row `row` of key head `head`, from host copies of table, lens
+ * and cu (data is not read). out: int64 [3] = {sequence, position, byte offset of its tile}; sequence -1
+ * behind the last one, offset -1 where the row has no place. */
+rot_status kv4_slot(const rot_kv4_cache* cache, const rot_kv4_seqs* seqs, int64_t row, int head, int64_t* out);
+
+/* Synchronise the current device and report device-side errors recorded since the last call: bounded
+ * waits that gave up (ROT_ETIMEOUT) and page tables that named no page (ROT_EINVAL); clears the record. */
 rot_status rot_check_device(void);
 
 /* Testing hook for the bounded-wait failure path (the pages have no counterpart). Every

@@ -21,4 +21,4 @@ Parity status of each function is listed in the module docstrings; every functio
 here is pinned by a ``-m "not gpu"`` test in ``tests/test_oracle_pins.py`` except
 where a docstring says "parity unpinned".
 """
-from . import hadamard, harp, quant, linear  # noqa: F401
+from . import hadamard, harp, quant, linear, kv4  # noqa: F401

@@ -1,0 +1,188 @@
+"""The 4-bit paged key/value cache and the attention over it, fp64.
+
+Sources: HARP abstract and Hadamard-Int4-Accuracy wiki (Hypothesis): an orthonormal rotation spreads
+outliers over the group scales and cancels in products, (T q).(T k) = q.k; the quantiser is that of
+``oracle.quant`` (wiki, Method). The tile layout is the one ``include/rot_b200.h`` documents at
+``rot_kv4_cache``; here it is written as index formulas, byte by byte.
+
+``Cache`` holds codes and scales in natural order [pages, page, heads, ...]; ``to_bytes`` / ``from_bytes``
+convert to and from the library's tiles. ``attention`` is the definition in float64.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+from . import hadamard as Hd
+from . import quant as Q
+
+
+def tile_bytes(D: int, G: int) -> int:
+    return 32 * D + 128 * (D // G)
+
+
+def nibble_of_key(t, d, D: int):
+    """Index of the 4-bit code of coordinate d of token t (0..31) among the tile's key codes."""
+    c, j, i = d % 32 // 8, d // 32, d % 8
+    return ((t * 4 + c) * (D // 32) + j) * 8 + i
+
+
+def nibble_of_value(t, d, D: int):
+    """The same among the tile's value codes."""
+    s, h, c, b = t // 16, t % 16 // 8, t % 8 // 2, t % 2
+    r, j, i = d % 32 // 4, d // 32, d % 4
+    return (((((s * 2 + h) * 8 + r) * 4 + c) * 2 + b) * (D // 32) + j) * 4 + i
+
+
+def scale_of_key(t, g, NG: int):
+    """Index of the scale of group g of token t among the tile's key scales."""
+    return t * NG + g
+
+
+def scale_of_value(t, g, NG: int):
+    return (t // 2 * NG + g) * 2 + t % 2
+
+
+def _indices(D: int, G: int):
+    t, d, g = np.arange(32)[:, None], np.arange(D)[None], np.arange(D // G)[None]
+    NG = D // G
+    return ((nibble_of_key(t, d, D), scale_of_key(t, g, NG)), (nibble_of_value(t, d, D), scale_of_value(t, g, NG)))
+
+
+def pack_tile(kc, ks, vc, vs, G: int) -> np.ndarray:
+    """One tile's bytes from codes [32, D] and binary16 scales [32, NG] of keys and values."""
+    D = kc.shape[1]
+    out = np.zeros(tile_bytes(D, G), dtype=np.uint8)
+    codes, scales = [], []
+    for (nib, sc), code, scale in zip(_indices(D, G), (kc, vc), (ks, vs)):
+        n = np.zeros(32 * D, dtype=np.uint8)
+        n[nib.ravel()] = np.asarray(code).astype(np.int64).ravel() & 15
+        codes.append(n[0::2] | (n[1::2] << 4))
+        s = np.zeros(32 * (D // G), dtype=np.float16)
+        s[sc.ravel()] = np.asarray(scale, dtype=np.float16).ravel()
+        scales.append(s.view(np.uint8))
+    out[:] = np.concatenate(codes + scales)
+    return out
+
+
+def unpack_tile(tile: np.ndarray, D: int, G: int):
+    """(key codes int8 [32, D], key scales fp16 [32, NG], value codes, value scales) of a tile's bytes."""
+    tile = np.ascontiguousarray(tile)
+    half, ns = 16 * D, 64 * (D // G)
+    parts = []
+    for k, (nib, sc) in enumerate(_indices(D, G)):
+        b = tile[k * half:(k + 1) * half]
+        n = np.stack([b & 15, b >> 4], 1).ravel().astype(np.int8)
+        n = np.where(n > 7, n - 16, n).astype(np.int8)
+        s = tile[2 * half + k * ns:2 * half + (k + 1) * ns].copy().view(np.float16)
+        parts += [n[nib], s[sc]]
+    return tuple(parts)
+
+
+def quantise_rows(x: np.ndarray, G: int, signs=None, rotate: bool = True):
+    """Codes int8 [n, D] and scales fp16 [n, NG] of rows x [n, D]: the rotation in fp64, then
+    ``oracle.quant.quantize`` (int4)."""
+    x = np.asarray(x, dtype=np.float64)
+    return Q.quantize(Hd.rht_apply(x, signs) if rotate else x, 4, G)
+
+
+def dequantise(codes: np.ndarray, scales: np.ndarray, G: int) -> np.ndarray:
+    """code * scale in fp64 over the last axis."""
+    s = np.repeat(np.asarray(scales, dtype=np.float16).astype(np.float64), G, axis=-1)
+    with np.errstate(invalid="ignore"):
+        return np.asarray(codes, dtype=np.float64) * s
+
+
+def positions(lens, cu, total: int):
+    """(sequence, position) of each packed row; sequence -1 behind the last one. cu None: one row each."""
+    cu = np.arange(len(lens) + 1) if cu is None else np.asarray(cu)
+    out = []
+    for row in range(total):
+        seq = -1
+        for b in range(len(lens)):
+            if cu[b] <= row < cu[b + 1]:
+                seq = b
+        out.append((seq, int(lens[seq]) - int(cu[seq + 1] - row) if seq >= 0 else -1))
+    return out
+
+
+def attention(q: np.ndarray, keys, values, lens, cu, *, scale: float, causal: bool = True, window: int = 0,
+              absent=None):
+    """out [T, Hq, D] in fp64 (NaN rows: behind the last sequence). q: [T, Hq, D]; keys / values: for each
+    sequence [length, heads, D] in q's basis; absent: for each sequence a bool [length] of tokens that have
+    no page and are not attended to, or None."""
+    T, Hq, D = q.shape
+    out = np.full((T, Hq, D), np.nan)
+    for row, (b, pos) in enumerate(positions(lens, cu, T)):
+        if b < 0:
+            continue
+        n = max(int(lens[b]), 0)
+        x = np.arange(n)
+        seen = np.ones(n, dtype=bool)
+        if causal:
+            seen &= x <= pos
+        if window:
+            seen &= x > pos - window
+        if absent is not None:
+            seen &= ~absent[b]
+        share = Hq // keys[b].shape[1] if n else 1
+        for h in range(Hq):
+            if not seen.any():
+                out[row, h] = 0.0
+                continue
+            z = keys[b][seen, h // share] @ q[row, h] * scale
+            p = np.exp(z - z.max())
+            out[row, h] = (p[:, None] * values[b][seen, h // share]).sum(0) / p.sum()
+    return out
+
+
+def attention_bound(q, keys, values, lens, cu, *, scale: float, causal: bool = True, window: int = 0,
+                    unrotate: bool = False, absent=None) -> np.ndarray:
+    """Largest error of each element of the library's output against ``attention`` in the cache's basis
+    (q, keys, values as for ``attention``), from the roundings that the kernel makes:
+
+    * the query, to binary16 after an exact power-of-two scaling: 2^-11 of each coordinate (a coordinate
+      below 2^-28 of the row's largest: 2^-39 of that, absorbed), and fp32 sums, (D + 8) 2^-23 of their
+      terms' magnitudes (code offsets included: |q| 15 s against |q| 7 s); so a logit is off by at most
+      d = scale sum |q| |k'| (2^-11 + (D + 8) 2^-23), |k'| = |k| + 8 s <= 16 s.
+    * a probability: relative exp(2 d) - 1 for d on both sides of the division, 2^-11 to binary16, 2^-11
+      for its product with the value scale, 2^-20 for exp2 and the joins
+    * fp32 sums over the tokens, of terms of up to 16 value scales: (n / 16 + D + 16) 2^-22
+    * back through U^T (unrotate): every coordinate gets at most sum_d |e_d| / sqrt(D)
+
+    The caller adds the output's own rounding to bf16, 2^-8 of the value.
+    """
+    T, Hq, D = q.shape
+    bound = np.zeros((T, Hq, D))
+    for row, (b, pos) in enumerate(positions(lens, cu, T)):
+        if b < 0:
+            continue
+        n = max(int(lens[b]), 0)
+        x = np.arange(n)
+        seen = np.ones(n, dtype=bool)
+        if causal:
+            seen &= x <= pos
+        if window:
+            seen &= x > pos - window
+        if absent is not None:
+            seen &= ~absent[b]
+        if not seen.any():
+            continue
+        share = Hq // keys[b].shape[1]
+        for h in range(Hq):
+            k, v = np.abs(keys[b][seen, h // share]), np.abs(values[b][seen, h // share])
+            z = keys[b][seen, h // share] @ q[row, h] * scale
+            p = np.exp(z - z.max())
+            p /= p.sum()
+            aq = np.abs(q[row, h])
+            # 16 scales of a group are at most 16 / 7 of its largest value (its code is 7), so of the token's
+            kmax = k.max(1, keepdims=True) * (16.0 / 7.0) * 1.001
+            d = scale * (k @ aq * 2.0 ** -11 + (kmax * aq).sum(1) * (D + 8) * 2.0 ** -23)
+            rel = np.expm1(2 * d.max() + 2 * d) + 2 * 2.0 ** -11 + 2.0 ** -20
+            vmax = np.nanmax(v, 1, keepdims=True, initial=0.0) * (16.0 / 7.0) * 1.001
+            e = (p * rel) @ v + np.broadcast_to((p @ vmax) * (n / 16 + D + 16) * 2.0 ** -22, (D,))
+            # products that fall below binary16's normal range, against the largest scale in sight
+            e = e + n * 2.0 ** -26 * np.nanmax(v, initial=0.0) / 7.0
+            if unrotate:
+                e = np.broadcast_to(e.sum() / np.sqrt(D), (D,))
+            bound[row, h] = e
+    return bound

@@ -1,0 +1,240 @@
+"""CPU checks of the 4-bit key/value cache: pins of its oracle, the addressing that the kernels share, and
+the refusals of its entry points."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from kv4_scene import Scene, signs_of
+from oracle import hadamard as Hd
+from oracle import kv4 as O
+
+SHAPES = [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (256, 32), (256, 64), (256, 128), (256, 256)]
+
+
+# ----------------------------------------------------------------------------- oracle pins
+
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_tile_places_are_a_bijection(D, G):
+    t, d, g = np.arange(32)[:, None], np.arange(D)[None], np.arange(D // G)[None]
+    for n in (O.nibble_of_key(t, d, D), O.nibble_of_value(t, d, D)):
+        assert sorted(n.ravel()) == list(range(32 * D))
+    for n in (O.scale_of_key(t, g, D // G), O.scale_of_value(t, g, D // G)):
+        assert sorted(n.ravel()) == list(range(32 * (D // G)))
+
+
+def test_tile_bytes_by_hand():
+    """One code and one scale at a time against places written out by hand from the documented order."""
+    D, G = 128, 32
+    z, s = np.zeros((32, D), np.int8), np.zeros((32, 4), np.float16)
+    k = z.copy()
+    k[3, 32 * 2 + 8 * 1 + 5] = -3            # token 3, c = 1, j = 2, i = 5
+    tile = O.pack_tile(k, s, z, s, G)
+    assert tile[3 * 64 + 1 * 16 + 2 * 4 + 2] == 0xD0 and (tile != 0).sum() == 1
+    v = z.copy()
+    v[16 + 8 + 2 * 3 + 1, 32 * 1 + 4 * 6 + 2] = 7   # s = 1, h = 1, c = 3, b = 1, j = 1, r = 6, i = 2
+    tile = O.pack_tile(z, s, v, s, G)
+    assert tile[16 * D + 8 * D + 4 * D + 6 * 64 + 3 * 16 + 8 + 1 * 2 + 1] == 0x07 and (tile != 0).sum() == 1
+    w = s.copy()
+    w[5, 2] = 1.0
+    assert O.pack_tile(z, w, z, s, G)[32 * D + (5 * 4 + 2) * 2 + 1] == 0x3C
+    assert O.pack_tile(z, s, z, w, G)[32 * D + 256 + ((2 * 4 + 2) * 2 + 1) * 2 + 1] == 0x3C
+    assert O.tile_bytes(D, G) == 4608
+
+
+@pytest.mark.parametrize("D,G", SHAPES)
+def test_tile_round_trip(D, G):
+    g = np.random.default_rng(D + G)
+    kc, vc = (g.integers(-7, 8, (32, D)).astype(np.int8) for _ in range(2))
+    ks, vs = (g.random((32, D // G)).astype(np.float16) for _ in range(2))
+    for a, b in zip(O.unpack_tile(O.pack_tile(kc, ks, vc, vs, G), D, G), (kc, ks, vc, vs)):
+        assert np.array_equal(a, b)
+
+
+def test_attention_against_closed_forms():
+    g = np.random.default_rng(0)
+    v = g.standard_normal((9, 1, 4))
+    # equal keys: the mean of what is seen; one new token at the end, then three
+    k = np.ones((9, 1, 4))
+    q = g.standard_normal((1, 2, 4))
+    out = O.attention(q, [k], [v], [9], None, scale=0.5)
+    assert np.allclose(out[0, 1], v[:, 0].mean(0), atol=1e-12)
+    q = g.standard_normal((3, 1, 4))
+    out = O.attention(q, [k], [v], [9], [0, 3], scale=0.5, window=2)
+    for i, pos in enumerate((6, 7, 8)):
+        assert np.allclose(out[i, 0], v[pos - 1:pos + 1, 0].mean(0), atol=1e-12)
+    # two keys: the logistic function of the difference
+    k2, v2 = np.array([[[1.0]], [[3.0]]]), np.array([[[0.0]], [[1.0]]])
+    out = O.attention(np.array([[[0.7]]]), [k2], [v2], [2], None, scale=2.0)
+    assert np.isclose(out[0, 0, 0], 1 / (1 + np.exp(-2.0 * 0.7 * 2.0)))
+    # nothing seen, and rows behind the last sequence
+    out = O.attention(g.standard_normal((4, 1, 4)), [k[:1]], [v[:1]], [1], [0, 3], scale=1.0)
+    assert (out[:2] == 0).all() and np.allclose(out[2, 0], v[0, 0]) and np.isnan(out[3]).all()
+
+
+def test_rotation_cancels_in_the_products():
+    """(T q).(T k) = q.k and U^T sum p (U v) = sum p v: attention in the rotated basis is attention."""
+    g = np.random.default_rng(2)
+    D = 64
+    s = signs_of(D)
+    q, k, v = g.standard_normal((2, 4, D)), g.standard_normal((7, 2, D)), g.standard_normal((7, 2, D))
+    rot = lambda x, inv=False: Hd.rht_apply(x.reshape(-1, D), s, inverse=inv).reshape(x.shape)
+    a = O.attention(q, [k], [v], [7], [0, 2], scale=0.3)
+    b = rot(O.attention(rot(q), [rot(k)], [rot(v)], [7], [0, 2], scale=0.3), True)
+    assert np.allclose(a, b, atol=1e-12)
+
+
+# ----------------------------------------------------------------------------- addressing
+
+def _host_cache(lib, sc):
+    import torch
+    return lib.KV4Cache(torch.from_numpy(sc.data()), sc.D, sc.G)
+
+
+@pytest.mark.parametrize("lens,new,page", [
+    ([70, 1, 33, 0, 64], [3, 1, 33, 0, 2], 32),
+    ([257], [257], 96),
+    ([5, 40], [9, 2], 64),          # more new tokens than tokens: positions below zero
+    ([31, 32, 33], [0, 0, 1], 160),
+])
+def test_slots_match_the_oracle(lib, lens, new, page):
+    sc = Scene(lens, new, heads=3, page=page, seed=len(lens), spare=1) if all(n <= l for l, n in zip(lens, new)) else None
+    if sc is None:
+        sc = Scene(lens, [0] * len(lens), heads=3, page=page)
+        sc.new = np.asarray(new, np.int32)
+        sc.cu = np.concatenate([[0], np.cumsum(sc.new)]).astype(np.int32)
+        sc.T = int(sc.cu[-1])
+    cache = _host_cache(lib, sc)
+    total = sc.T + 3
+    want = O.positions(sc.lens, sc.cu, total)
+    for row in range(total):
+        for h in range(3):
+            seq, pos, at = lib.kv4_slot(cache, sc.table, sc.lens, sc.cu, row, h, total=total)
+            assert seq == want[row][0]
+            if seq < 0:
+                assert at == -1
+                continue
+            assert pos == want[row][1]
+            if pos < 0:
+                assert at == -1
+            else:
+                tile = (sc.table[seq, pos // page] * 3 + h) * (page // 32) + pos % page // 32
+                assert at == tile * sc.tb
+
+
+def test_slots_refuse_pages_outside_the_cache(lib):
+    sc = Scene([100, 64], [1, 1], page=32, spare=0)
+    cache = _host_cache(lib, sc)
+    pages = sc.pages
+    for bad in (-1, pages, pages + 1, -2 ** 31, 2 ** 31 - 1):
+        table = sc.table.copy()
+        table[0, 3] = bad
+        assert lib.kv4_slot(cache, table, sc.lens, None, 0, 1)[2] == -1
+        assert lib.kv4_slot(cache, table, sc.lens, None, 1, 1)[2] >= 0
+    # lengths past the table's columns, and below zero
+    for n in (4 * 32 + 1, 2 ** 31 - 1, 0, -1, -2 ** 31):
+        assert lib.kv4_slot(cache, sc.table, [n, 64], None, 0, 0)[2] == -1
+
+
+def test_slot_offsets_pass_32_bits(lib):
+    """A page far into a large cache: the offset is 64-bit arithmetic (no memory is touched)."""
+    tb = lib.KV4Cache.tile_bytes(128, 32)
+    cache = lib.KV4Cache.__new__(lib.KV4Cache)
+    cache._c = lib._KV4CacheStruct(None, 16 * tb, 3_000_000, 64, 8, 128, 32, None, None)
+    seq, pos, at = lib.kv4_slot(cache, [[2_999_999]], [64], None, 0, 7)
+    assert at == (2_999_999 * 16 + 15) * tb and at > 2 ** 37
+
+
+# ----------------------------------------------------------------------------- refusals
+
+def test_cache_constructor_refusals(lib):
+    import torch
+    ok = torch.zeros((4, 2, 1, lib.KV4Cache.tile_bytes(64, 32)), dtype=torch.uint8)
+    lib.KV4Cache(ok, 64, 32)
+    for data, D, G in ((ok, 64, 64), (ok, 96, 32), (ok, 64, 16), (ok, 64, 128), (ok[0], 64, 32), (ok.to(torch.int8), 64, 32),
+                       (ok.transpose(1, 2).contiguous().transpose(1, 2).expand(4, 2, 1, -1)[:, :, :, ::2], 64, 32),
+                       (ok[:, :0], 64, 32), (ok.permute(0, 2, 1, 3).expand(-1, 2, -1, -1), 64, 32)):
+        with pytest.raises(lib.RotError) as e:
+            lib.KV4Cache(data, D, G)
+        assert e.value.status == lib.ROT_EINVAL
+    with pytest.raises(lib.RotError):
+        lib.KV4Cache.empty(4, 33, 2, 64, 32, device="cpu")
+
+
+def test_calls_refuse_host_tensors(lib):
+    import torch
+    sc = Scene([5], [1])
+    cache = _host_cache(lib, sc)
+    t = torch.zeros((1, 2, 64))
+    for call in (lambda: lib.kv4_append(cache, t, t, torch.zeros(1, 1).int(), torch.ones(1).int()),
+                 lambda: lib.kv4_read(cache, torch.zeros(1, 1).int(), torch.ones(1).int()),
+                 lambda: lib.kv4_attention(t, cache, torch.zeros(1, 1).int(), torch.ones(1).int())):
+        with pytest.raises((lib.RotError, RuntimeError, AssertionError)):
+            call()
+
+
+def _structs(lib, **kw):
+    buf = (C.c_uint8 * 4096)()
+    at = (C.addressof(buf) + 15) // 16 * 16
+    c = dict(data=at, page_stride=2 * 2304, pages=4, page=32, heads=2, D=64, G=32, k_plan=None, v_plan=None)
+    s = dict(table=at, table_stride=3, table_pages=3, lens=at, cu=None, B=2, T=2)
+    a = dict(q_dtype=lib.ROT_BF16, q_token=256, q_head=64, Hq=4, scale=0.125, causal=1, window=0, max_new=1, max_len=64,
+             q=at, out=at, ws=at, nws=1 << 40)
+    for k, v in kw.items():
+        for d in (c, s, a):
+            if k in d:
+                d[k] = v
+    return buf, lib._KV4CacheStruct(*c.values()), lib._KV4SeqsStruct(*s.values()), a
+
+
+@pytest.mark.parametrize("kw", [
+    dict(D=96), dict(D=32), dict(G=16), dict(G=128), dict(G=48), dict(page=0), dict(page=48), dict(page=-32),
+    dict(heads=0), dict(pages=-1), dict(page_stride=4592), dict(page_stride=4617), dict(data=None), dict(data=8 + 16 * 100),
+    dict(B=-1), dict(T=-1), dict(T=3), dict(table_stride=2), dict(table_pages=-1), dict(lens=None), dict(table=None),
+    dict(T=2 ** 31, cu=16), dict(q_dtype=2), dict(Hq=3), dict(Hq=0), dict(Hq=-2), dict(scale=float("nan")),
+    dict(scale=float("inf")), dict(window=-1), dict(window=5, causal=0), dict(max_new=-1), dict(max_len=-1),
+    dict(q=None), dict(out=None), dict(q_token=257), dict(q_head=63), dict(q_head=68), dict(q_token=-256),
+    dict(max_len=1 << 20, ws=None), dict(max_len=1 << 20, nws=16), dict(max_len=1 << 20, ws=24),
+], ids=str)
+def test_attention_refusals_without_a_device(lib, kw):
+    buf, c, s, a = _structs(lib, **kw)
+    st = lib._lib.kv4_attention(C.byref(c), C.byref(s), a["q"], a["q_dtype"], a["q_token"], a["q_head"], a["Hq"], a["scale"],
+                                a["causal"], a["window"], a["max_new"], a["max_len"], a["out"], a["ws"], a["nws"], None)
+    assert st in (lib.ROT_EINVAL, lib.ROT_EUNSUPPORTED) and "kv4_attention" in lib.last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(dtype=7), dict(k=None), dict(v=None), dict(token=130 + 1), dict(head=32), dict(head=65)],
+                         ids=str)
+def test_append_refusals_without_a_device(lib, kw):
+    buf, c, s, a = _structs(lib)
+    p = dict(k=a["q"], v=a["q"], token=128, head=64, dtype=lib.ROT_BF16) | kw
+    st = lib._lib.kv4_append(C.byref(c), C.byref(s), p["k"], p["token"], p["head"], p["v"], p["token"], p["head"], p["dtype"], None)
+    assert st == lib.ROT_EINVAL and "kv4_append" in lib.last_error()
+    if "token" not in kw and "head" not in kw:
+        st = lib._lib.kv4_read(C.byref(c), C.byref(s), 0, p["k"], p["v"], p["dtype"], None)
+        assert st == lib.ROT_EINVAL and "kv4_read" in lib.last_error()
+
+
+def test_null_structs_and_empty_calls(lib):
+    buf, c, s, a = _structs(lib)
+    assert lib._lib.kv4_append(None, C.byref(s), a["q"], 128, 64, a["q"], 128, 64, 1, None) == lib.ROT_EINVAL
+    assert lib._lib.kv4_read(C.byref(c), None, 0, a["q"], a["q"], 1, None) == lib.ROT_EINVAL
+    # no rows: nothing is launched, so nothing is needed
+    buf, c, s, a = _structs(lib, T=0, B=0, lens=None, table=None)
+    assert lib._lib.kv4_append(C.byref(c), C.byref(s), None, 0, 0, None, 0, 0, 1, None) == lib.ROT_OK
+    assert lib._lib.kv4_read(C.byref(c), C.byref(s), 0, None, None, 1, None) == lib.ROT_OK
+
+
+def test_workspace_covers_the_split(lib):
+    """A length is split only where the sequences leave the GPU idle, and the workspace holds every part."""
+    import torch
+    cache = lib.KV4Cache(torch.zeros((1, 8, 1, lib.KV4Cache.tile_bytes(128, 32)), dtype=torch.uint8), 128, 32)
+    size = lambda B, T, n, m, **kw: lib.kv4_attention_workspace(cache, B, T, 32, max_new=n, max_len=m, **kw)
+    assert size(1, 1, 1, 64) == 0 and size(4096, 4096, 1, 1 << 17) == 0
+    long = size(1, 1, 1, 1 << 17)
+    assert long > 0 and long % (32 * 130 * 4) == 0
+    assert size(1, 1, 1, 1 << 17, window=64) == 0
+    assert size(0, 0, 1, 1 << 17) == 0
+    for bad in (dict(B=-1), dict(T=-1), dict(n=-1), dict(m=-1)):
+        with pytest.raises(lib.RotError):
+            size(**(dict(B=1, T=1, n=1, m=64) | bad))
