@@ -13,6 +13,7 @@ Names follow the C ABI: ``Plan`` (rot_plan_create / rot_plan_destroy), ``rot_app
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -526,53 +527,95 @@ class KV4Cache:
         data = torch.empty((pages, heads, page // 32, cls.tile_bytes(D, G)), dtype=torch.uint8, device=device)
         return cls(data, D, G, k_plan=k_plan, v_plan=v_plan)
 
-    def _struct(self, current: int):
-        """The C view, checked against the current device and with the plans as they are now."""
-        if not self.data.is_cuda:
+    def _struct(self):
+        """(C view, device index): checked against the current device and with the plans as they are now."""
+        import torch
+        index = self.data.get_device()
+        if index < 0:
             raise RotError(ROT_EINVAL, f"the cache must be on a CUDA device, not {self.data.device}")
-        _check_device(self.data.device.index, current, "the cache")
+        _check_device(index, torch.cuda.current_device(), "the cache")
+        c = self._c
         for name, plan in (("k_plan", self.k_plan), ("v_plan", self.v_plan)):
-            if plan is not None and not plan.handle.value:
+            if plan is None:
+                setattr(c, name, None)
+            elif not plan.handle.value:
                 raise RotError(ROT_EINVAL, f"the cache's {name} was closed")
-        self._c.k_plan = self.k_plan.handle if self.k_plan is not None else None
-        self._c.v_plan = self.v_plan.handle if self.v_plan is not None else None
-        return C.byref(self._c)
+            else:
+                setattr(c, name, plan.handle.value)
+        return C.byref(c), index
 
 
-def _kv4_seqs(table, lens, cu, T: int):
+def _kv4_on(t, name: str, index: int):
+    """A torch tensor on the device of that index, which is the current one (see _arg)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise RotError(ROT_EINVAL, f"{name} must be a torch tensor")
+    at = t.get_device()
+    if at != index:
+        if at < 0:
+            raise RotError(ROT_EINVAL, f"{name} must be on a CUDA device, not {t.device}")
+        _check_device(at, index, name)
+
+
+def _kv4_seqs(table, lens, cu, T: int, index: int):
     """Checked rot_kv4_seqs of page table, lengths and row offsets."""
     import torch
-    pl = _arg(lens, "lens", dtype=torch.int32)
-    if lens.dim() != 1:
-        raise RotError(ROT_EINVAL, "lens must be 1-D")
+    i32 = torch.int32
+    _kv4_on(lens, "lens", index)
+    if lens.dim() != 1 or lens.dtype != i32 or not lens.is_contiguous():
+        raise RotError(ROT_EINVAL, "lens must be a contiguous 1-D int32 tensor")
     B = lens.shape[0]
-    pt = _arg(table, "table", dtype=torch.int32, strided_rows=True)
-    if table.dim() != 2 or table.shape[0] != B:
-        raise RotError(ROT_EINVAL, f"table must be 2-D with one row for each of {B} sequences")
+    _kv4_on(table, "table", index)
+    if table.dim() != 2 or table.shape[0] != B or table.dtype != i32:
+        raise RotError(ROT_EINVAL, f"table must be a 2-D int32 tensor with one row for each of {B} sequences")
+    cols = table.shape[1]
+    step, unit = table.stride()
+    if cols > 1 and unit != 1:
+        raise RotError(ROT_EINVAL, "table must have unit stride along its rows")
     pc = None
     if cu is not None:
-        pc = _arg(cu, "cu", dtype=torch.int32, shape=(B + 1,))
+        _kv4_on(cu, "cu", index)
+        if cu.dim() != 1 or cu.shape[0] != B + 1 or cu.dtype != i32 or not cu.is_contiguous():
+            raise RotError(ROT_EINVAL, f"cu must be a contiguous int32 tensor of {B + 1} offsets")
+        pc = cu.data_ptr()
     elif T != B:
         raise RotError(ROT_EINVAL, f"without cu there is one new token per sequence: got {T} rows for {B} sequences")
-    cols = table.shape[1]
-    return C.byref(_KV4SeqsStruct(pt, max(table.stride(0), cols) if B > 1 else cols, cols, pl, pc, B, T))
+    return C.byref(_KV4SeqsStruct(table.data_ptr(), step if B > 1 and step > cols else cols, cols, lens.data_ptr(), pc, B, T))
 
 
-def _kv4_rows(t, name: str, heads, D: int):
-    """Checked address and strides of rows [T, heads, D] with unit stride along D."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise RotError(ROT_EINVAL, f"{name} must be a torch tensor on a CUDA device")
-    _check_device(t.device.index, torch.cuda.current_device(), name)
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise RotError(ROT_EINVAL, f"{name} must be bf16 or fp32, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
-        raise RotError(ROT_EINVAL, f"{name} must have shape [T, {'Hq' if heads is None else heads}, {D}], got {tuple(t.shape)}")
-    if t.numel() and t.stride(2) != 1:
+def _kv4_rows(t, name: str, heads, D: int, index: int):
+    """Checked address, strides and dtype code of rows [T, heads, D] with unit stride along D."""
+    _kv4_on(t, name, index)
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads):
+        raise RotError(ROT_EINVAL, f"{name} must have shape [T, {'Hq' if heads is None else heads}, {D}], got {tuple(shape)}")
+    try:
+        kind = _dtype_code(t)
+    except TypeError:
+        raise RotError(ROT_EINVAL, f"{name} must be bf16 or fp32, got {t.dtype}") from None
+    token, head, unit = t.stride()
+    if unit != 1 and t.numel():
         raise RotError(ROT_EINVAL, f"{name} must have unit stride along its last dimension")
     # (the stride of a dimension of one element may be anything)
-    head = t.stride(1) if t.shape[1] > 1 else D
-    return C.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else head * t.shape[1], head
+    if shape[1] <= 1:
+        head = D
+    return t.data_ptr(), token if shape[0] > 1 else head * shape[1], head, kind
+
+
+def _kv4_out(t, name: str, dtypes, shape, index: int):
+    """Checked address of a dense output."""
+    _kv4_on(t, name, index)
+    if t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_contiguous():
+        raise RotError(ROT_EINVAL, f"{name} must be a contiguous {' or '.join(map(str, dtypes))} tensor of shape {shape}, "
+                                   f"got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _kv4_stream(stream, index: int):
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _kv4_empty(shape, dtype, device, stream):
@@ -589,14 +632,13 @@ def kv4_append(cache: KV4Cache, k, v, table, lens, cu=None, *, stream=None) -> N
     """Rotate, quantise and write the new tokens' keys and values (bf16 or fp32 [T, heads, D], any token and
     head strides) into the cache. table int32 [B, pages of a sequence], lens int32 [B] with the new tokens
     among them, cu int32 [B + 1] the offsets of each sequence's rows (None: one new token each)."""
-    import torch
-    cs = cache._struct(torch.cuda.current_device())
-    pk, kt, kh = _kv4_rows(k, "k", cache.heads, cache.D)
-    pv, vt, vh = _kv4_rows(v, "v", cache.heads, cache.D)
-    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+    cs, index = cache._struct()
+    pk, kt, kh, kind = _kv4_rows(k, "k", cache.heads, cache.D, index)
+    pv, vt, vh, vkind = _kv4_rows(v, "v", cache.heads, cache.D, index)
+    if kind != vkind or k.shape[0] != v.shape[0]:
         raise RotError(ROT_EINVAL, "k and v must have the same dtype and number of rows")
-    ss = _kv4_seqs(table, lens, cu, k.shape[0])
-    _check(_lib.kv4_append(cs, ss, pk, kt, kh, pv, vt, vh, _dtype_code(k), _stream(stream)))
+    ss = _kv4_seqs(table, lens, cu, k.shape[0], index)
+    _check(_lib.kv4_append(cs, ss, pk, kt, kh, pv, vt, vh, kind, _kv4_stream(stream, index)))
 
 
 def kv4_read(cache: KV4Cache, table, lens, cu=None, *, total=None, inverse: bool = False, out_dtype=None, out=None,
@@ -605,35 +647,36 @@ def kv4_read(cache: KV4Cache, table, lens, cu=None, *, total=None, inverse: bool
     [total, heads, D], total the packed rows (default: one for each sequence). Stored basis, or with
     inverse the original one; bf16 (default) or fp32. Rows behind the last sequence are left as they were."""
     import torch
-    cs = cache._struct(torch.cuda.current_device())
+    cs, index = cache._struct()
     T = int(total) if total is not None else lens.shape[0]
     shape = (T, cache.heads, cache.D)
     if out is None:
-        kind = out_dtype or torch.bfloat16
-        out = tuple(_kv4_empty(shape, kind, cache.data.device, stream) for _ in range(2))
-    k, v = out
-    pk = _arg(k, "out[0]", dtype=(torch.float32, torch.bfloat16), shape=shape)
-    pv = _arg(v, "out[1]", dtype=k.dtype, shape=shape)
-    ss = _kv4_seqs(table, lens, cu, T)
-    _check(_lib.kv4_read(cs, ss, int(inverse), pk, pv, _dtype_code(k), _stream(stream)))
+        both = _kv4_empty((2, *shape), out_dtype or torch.bfloat16, cache.data.device, stream)
+        k, v = both.unbind(0)
+    else:
+        k, v = out
+    pk = _kv4_out(k, "out[0]", (torch.float32, torch.bfloat16), shape, index)
+    pv = _kv4_out(v, "out[1]", (k.dtype,), shape, index)
+    ss = _kv4_seqs(table, lens, cu, T, index)
+    _check(_lib.kv4_read(cs, ss, int(inverse), pk, pv, _dtype_code(k), _kv4_stream(stream, index)))
     return k, v
 
 
-def _kv4_sizes(cache, table, max_new, max_len, cu, T: int):
-    """The sizes that a launch is laid out for, where the caller names none."""
-    if max_new is None:
-        max_new = 1 if cu is None else T
-    if max_len is None:
-        max_len = table.shape[1] * cache.page
-    return int(max_new), int(max_len)
+@functools.lru_cache(maxsize=1024)
+def _kv4_workspace_bytes(shape, index: int, B: int, T: int, Hq: int, window: int, max_new: int, max_len: int) -> int:
+    """kv4_attention_workspace of a cache's shape (D, G, heads) on a device: a function of these numbers alone."""
+    D, G, heads = shape
+    c = _KV4CacheStruct(None, heads * KV4Cache.tile_bytes(D, G), 0, 32, heads, D, G, None, None)
+    n = C.c_size_t()
+    _check(_lib.kv4_attention_workspace(C.byref(c), B, T, Hq, window, max_new, max_len, C.byref(n)))
+    return int(n.value)
 
 
 def kv4_attention_workspace(cache: KV4Cache, B: int, T: int, Hq: int, *, max_new: int, max_len: int,
                             window: int = 0) -> int:
     """Bytes of the workspace that kv4_attention needs for these sizes (0: none)."""
-    n = C.c_size_t()
-    _check(_lib.kv4_attention_workspace(C.byref(cache._c), B, T, Hq, window, max_new, max_len, C.byref(n)))
-    return int(n.value)
+    return _kv4_workspace_bytes((cache.D, cache.G, cache.heads), max(cache.data.get_device(), 0), B, T, Hq, window, max_new,
+                                max_len)
 
 
 def kv4_attention(q, cache: KV4Cache, table, lens, cu=None, *, max_new=None, max_len=None, scale=None,
@@ -644,21 +687,31 @@ def kv4_attention(q, cache: KV4Cache, table, lens, cu=None, *, max_new=None, max
     (the most new tokens and the longest length of a sequence) size the launch: give them where they are
     known, since they cannot be read off device tensors. workspace: uint8, allocated here if not given."""
     import torch
-    cs = cache._struct(torch.cuda.current_device())
-    pq, qt, qh = _kv4_rows(q, "q", None, cache.D)
+    cs, index = cache._struct()
+    D = cache.D
+    pq, qt, qh, kind = _kv4_rows(q, "q", None, D, index)
     T, Hq = q.shape[0], q.shape[1]
-    ss = _kv4_seqs(table, lens, cu, T)
-    max_new, max_len = _kv4_sizes(cache, table, max_new, max_len, cu, T)
-    n = C.c_size_t()
-    _check(_lib.kv4_attention_workspace(cs, lens.shape[0], T, Hq, window, max_new, max_len, C.byref(n)))
+    ss = _kv4_seqs(table, lens, cu, T, index)
+    if max_new is None:
+        max_new = 1 if cu is None else T
+    if max_len is None:
+        max_len = table.shape[1] * cache.page
+    need = _kv4_workspace_bytes((D, cache.G, cache.heads), index, lens.shape[0], T, Hq, window, max_new, max_len)
+    shape = (T, Hq, D)
     if out is None:
-        out = _kv4_empty((T, Hq, cache.D), torch.bfloat16, q.device, stream)
-    po = _arg(out, "out", dtype=torch.bfloat16, shape=(T, Hq, cache.D))
-    if workspace is None and n.value:
-        workspace = _kv4_empty((n.value,), torch.uint8, q.device, stream)
-    pw, nw = (_arg(workspace, "workspace", dtype=torch.uint8), workspace.numel()) if workspace is not None else (None, 0)
-    _check(_lib.kv4_attention(cs, ss, pq, _dtype_code(q), qt, qh, Hq, cache.D ** -0.5 if scale is None else scale,
-                              int(causal), window, max_new, max_len, po, pw, nw, _stream(stream)))
+        out = _kv4_empty(shape, torch.bfloat16, q.device, stream)
+    po = _kv4_out(out, "out", (torch.bfloat16,), shape, index)
+    pw, nw = None, 0
+    if workspace is not None:
+        _kv4_on(workspace, "workspace", index)
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise RotError(ROT_EINVAL, "workspace must be a contiguous uint8 tensor")
+        pw, nw = workspace.data_ptr(), workspace.numel()
+    elif need:
+        workspace = _kv4_empty((need,), torch.uint8, q.device, stream)
+        pw, nw = workspace.data_ptr(), need
+    _check(_lib.kv4_attention(cs, ss, pq, kind, qt, qh, Hq, D ** -0.5 if scale is None else scale, causal, window,
+                              max_new, max_len, po, pw, nw, _kv4_stream(stream, index)))
     return out
 
 

@@ -22,6 +22,8 @@
 // P and P * scale (binary16, 2^-11 / 2 each); sums, maxima and logits are fp32. bf16 for P would round at
 // 2^-8 / 2, as coarse as the bf16 output itself.
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "kv4.cuh"
 
@@ -68,9 +70,32 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// offset nibbles u = q + 8 of two packed halves as binary16 subnormals: bits 0..3 and bits 4..7
-__device__ __forceinline__ uint32_t lo_nib(uint32_t w) { return (w & 0x000F000Fu) ^ 0x00080008u; }
-__device__ __forceinline__ uint32_t hi_nib(uint32_t w) { return (w & 0x00F000F0u) ^ 0x00800080u; }
+// offset nibbles u = q + 8 of two packed halves as binary16 subnormals: bits 0..3 (u 2^-24) and bits 4..7
+// (16 u 2^-24), one three-input operation each: (w & mask) ^ flip, mask and flip in registers
+struct Nibbles {
+  uint32_t lo_mask, lo_flip, hi_mask, hi_flip;
+  // Loaded from shared memory: an instruction has room for one immediate or uniform register, and a constant
+  // that the compiler knows is copied anew for every use (64 of 640 instructions per tile).
+  static __device__ __forceinline__ void store(uint32_t* to) {
+    to[0] = 0x000F000Fu;
+    to[1] = 0x00080008u;
+    to[2] = 0x00F000F0u;
+    to[3] = 0x00800080u;
+  }
+  __device__ __forceinline__ explicit Nibbles(uint32_t addr) {
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(lo_mask), "=r"(lo_flip), "=r"(hi_mask), "=r"(hi_flip) : "r"(addr));
+  }
+  __device__ __forceinline__ uint32_t lo(uint32_t w) const {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(w), "r"(lo_mask), "r"(lo_flip));
+    return d;
+  }
+  __device__ __forceinline__ uint32_t hi(uint32_t w) const {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(w), "r"(hi_mask), "r"(hi_flip));
+    return d;
+  }
+};
 
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -80,9 +105,14 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {  // drops NaN
-  const __half2 h = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+__device__ __forceinline__ uint32_t max_half2_nan(uint32_t a, uint32_t b) {
+  const __half2 h = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// all ones in the halves that hold an infinity or a NaN
+__device__ __forceinline__ uint32_t odd_halves(uint32_t x) {
+  return ((x & 0x7c00u) == 0x7c00u ? 0xffffu : 0u) | ((x & 0x7c000000u) == 0x7c000000u ? 0xffff0000u : 0u);
 }
 
 // n 32-bit words from shared memory with the widest loads
@@ -127,17 +157,21 @@ __device__ __forceinline__ void key_scales(uint32_t addr, float (&s)[NG]) {
     uint16_t h;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr));
     s[0] = __half2float(__ushort_as_half(h));
+    s[0] = fmaf(s[0], 0.0f, s[0]);
   } else {
     uint32_t w[NG / 2];
     lds<NG / 2>(addr, w);
 #pragma unroll
-    for (int i = 0; i < NG; ++i) s[i] = __half2float(__ushort_as_half((uint16_t)(w[i / 2] >> (16 * (i & 1)))));
+    for (int i = 0; i < NG / 2; ++i) {
+      __half2 h = *reinterpret_cast<const __half2*>(&w[i]);
+      h = __hfma2(h, __half2half2(__ushort_as_half(0)), h);
+      s[2 * i] = __low2float(h);
+      s[2 * i + 1] = __high2float(h);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < NG; ++i) s[i] = fmaf(s[i], 0.0f, s[i]);
 }
 
-constexpr int stages_of(int D) { return D == 256 ? 2 : D == 128 ? 3 : 4; }
+constexpr int stages_of(int D) { return D == 64 ? 3 : 2; }
 
 template <int D, int NG, int NT>
 struct Lay {
@@ -147,12 +181,14 @@ struct Lay {
   static constexpr int OUT = ROWS * (D + 4) * 4;               // a warp's O at the end, in place of its ring
   static constexpr int RING = ST * TILE > OUT ? ST * TILE : OUT;
   static constexpr int QF = NT * (D / 32) * 32 * 16;           // B fragments of Q: [nt][j][lane] 16 bytes
-  static constexpr int BIAS = ROWS * NG * 4;                   // -8 2^-24 sum q' per row and group
+  static constexpr int BIAS = ROWS * NG * 8;                   // -8 2^-24 sum q' per row and group, in quads
   static constexpr int O_Q = W * RING;
   static constexpr int O_BIAS = O_Q + QF;
   static constexpr int O_FAC = O_BIAS + BIAS;                  // per row: logit factor
-  static constexpr int O_ML = O_FAC + ROWS * 4;                // [W][ROWS][2]
-  static constexpr int O_BAR = O_ML + W * ROWS * 8;
+  static constexpr int O_SEEN = O_FAC + ROWS * 4;              // per row: the tokens that it sees
+  static constexpr int O_ML = O_SEEN + ROWS * 8;               // [W][ROWS][2]
+  static constexpr int O_NIB = O_ML + W * ROWS * 8;            // the constants of Nibbles
+  static constexpr int O_BAR = O_NIB + 16;
   static constexpr int SMEM = O_BAR + W * ST * 8;
 };
 
@@ -183,10 +219,19 @@ __device__ __forceinline__ void finish_row(const Params& p, float (&o)[D / 32], 
   else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+#ifndef KV4_HALF
+#define KV4_HALF 128
+#endif
+#ifndef KV4_B128
+#define KV4_B128 4
+#endif
+constexpr int ctas_of(int D, int NT) { return NT == 1 ? (D == 64 ? 4 : D == 128 ? KV4_B128 : 2) : (D == 64 ? 3 : 2); }
+
 template <int D, int NG, int NT, bool QF32>
-__global__ void __launch_bounds__(CTA) attention_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(CTA, ctas_of(D, NT)) attention_kernel(const __grid_constant__ Params p) {
   using L = Lay<D, NG, NT>;
   constexpr int J = D / 32, JG = J / NG, V = D / 32;
+  constexpr int HALVES = D * NT <= KV4_HALF ? 2 : 1;  // halves of a tile that are worked on together
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::O_BAR) + warp * L::ST;
@@ -195,6 +240,7 @@ __global__ void __launch_bounds__(CTA) attention_kernel(const __grid_constant__ 
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bars + s)) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid == 0) Nibbles::store(reinterpret_cast<uint32_t*>(smem + L::O_NIB));
   __syncwarp();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -218,6 +264,7 @@ __global__ void __launch_bounds__(CTA) attention_kernel(const __grid_constant__ 
   const uint32_t ring = smem_u32(smem) + warp * L::RING;
   float* qs_fac = reinterpret_cast<float*>(smem + L::O_FAC);
   float* qs_bias = reinterpret_cast<float*>(smem + L::O_BIAS);
+  int* qs_seen = reinterpret_cast<int*>(smem + L::O_SEEN);
   uint32_t* qs = reinterpret_cast<uint32_t*>(smem + L::O_Q);
   float* ml = reinterpret_cast<float*>(smem + L::O_ML);
 
@@ -326,52 +373,253 @@ __global__ void __launch_bounds__(CTA) attention_kernel(const __grid_constant__ 
       }
 #pragma unroll
       for (int x = 1; x < 32 / NG; x *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      if (lane % (32 / NG) == 0) qs_bias[rr * NG + lane / (32 / NG)] = sum * (-8.0f / 16777216.0f);
-      if (lane == 0) qs_fac[rr] = fac;
+      if (lane % (32 / NG) == 0) {
+        float* at = qs_bias + ((((rr >> 3) * NG + lane / (32 / NG)) * 4 + ((rr & 7) >> 1)) * 4 + (rr & 1));
+        at[0] = at[2] = sum * (-8.0f / 16777216.0f);
+      }
+      if (lane == 0) {
+        qs_fac[rr] = fac;
+        // the tokens that the row sees: [x, y)
+        int2 seen = make_int2(0, high);
+        if (row < n_rows) {
+          const int pos = pos0 + row / p.share;
+          if (p.causal) seen.y = min(high, pos + 1);
+          if (p.window) seen.x = max(0, pos - p.window + 1);
+        }
+        reinterpret_cast<int2*>(qs_seen)[rr] = seen;
+      }
     }
     __syncthreads();
 
     // ---- per thread: columns 2c, 2c + 1 of each n-tile
+    const Nibbles nib(smem_u32(smem + L::O_NIB));
     float fac[NT][2], ref[NT][2], sum[NT][2];
-    int seen_hi[NT][2], seen_lo[NT][2], all_hi = high, all_lo = low;
-    float o[NT][2 * J][4], ones[NT][NG][4], bias[NT][NG][2];
+    int all_hi = high, all_lo = low;
+    float o[NT][2 * J][4];
+    // Sums of P per group by an MMA with ones. Two groups share an accumulator: the first has its ones in the
+    // lower eight rows, the second in the upper ones.
+    constexpr int NP = (NG + 1) / 2;
+    float ones[NT][NP][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int rr = nt * 8 + 2 * c + k, row = row0 + rr;
+        const int rr = nt * 8 + 2 * c + k;
         fac[nt][k] = qs_fac[rr];
         ref[nt][k] = NINF;
         sum[nt][k] = 0.0f;
-        seen_hi[nt][k] = high;
-        seen_lo[nt][k] = 0;
-        if (row < n_rows) {
-          const int pos = pos0 + row / p.share;
-          if (p.causal) seen_hi[nt][k] = min(high, pos + 1);
-          if (p.window) seen_lo[nt][k] = max(0, pos - p.window + 1);
-          all_hi = min(all_hi, seen_hi[nt][k]);
-          all_lo = max(all_lo, seen_lo[nt][k]);
-        }
-#pragma unroll
-        for (int g = 0; g < NG; ++g) bias[nt][g][k] = qs_bias[rr * NG + g];
+        const int2 seen = reinterpret_cast<const int2*>(qs_seen)[rr];
+        all_lo = max(all_lo, seen.x);
+        all_hi = min(all_hi, seen.y);
       }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int m = 0; m < 2 * J; ++m)
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[nt][m][i] = 0.0f;
+        for (int q = 0; q < NP; ++q) ones[nt][q][i] = 0.0f;
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ones[nt][g][i] = 0.0f;
-    }
+        for (int m = 0; m < 2 * J; ++m) o[nt][m][i] = 0.0f;
+      }
 #pragma unroll
     for (int x = 1; x < 4; x *= 2) {
       all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, x));
       all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, x));
     }
+    uint32_t poison = 0;  // bit nt * NG + g: group g of row nt * 8 + r is NaN
     int vexp = -15;  // value scales are at most 2^vexp and enter the MMA as s 2^-vexp
+    uint32_t vdown = 0x78007800u;
+
+    // HALVES times sixteen tokens from `tk`, in shared memory at `tile`, from half `sub0` on. EDGE: some of
+    // them are outside the sequence, or out of reach of some row.
+    auto part = [&](auto edge_c, auto halves_c, uint32_t tile, int sub0, int tk) {
+      constexpr bool EDGE = decltype(edge_c)::value;
+      constexpr int HALVES = decltype(halves_c)::value;
+      // ---- S^T: tokens r, r + 8 of each half by columns 2c, 2c + 1
+      float e[HALVES][NT][4], S[HALVES][NT][4];
+      {
+        uint32_t kw[HALVES][2][J];
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf) {
+          lds<J>(tile + (16 * (sub0 + hf) + r) * (D / 2) + c * (D / 8), kw[hf][0]);
+          lds<J>(tile + (16 * (sub0 + hf) + r + 8) * (D / 2) + c * (D / 8), kw[hf][1]);
+        }
+        float s0[HALVES][NG], s1[HALVES][NG];
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf) {
+          key_scales<NG>(tile + 32 * D + (16 * (sub0 + hf) + r) * (2 * NG), s0[hf]);
+          key_scales<NG>(tile + 32 * D + (16 * (sub0 + hf) + r + 8) * (2 * NG), s1[hf]);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          float acc[HALVES][NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf) {
+              // -8 2^-24 sum q of the group, columns 2c, 2c + 1, 2c, 2c + 1: loaded as the accumulator
+              uint32_t bias[4];
+              lds<4>(smem_u32(qs_bias) + ((nt * NG + g) * 4 + c) * 16, bias);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[hf][nt][k] = __uint_as_float(bias[k]);
+            }
+#pragma unroll
+          for (int jj = 0; jj < JG; ++jj) {
+            const int j = g * JG + jj;
+            uint32_t qf[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) lds<4>(smem_u32(qs) + ((nt * J + j) * 32 + lane) * 16, qf[nt]);
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf) {
+              const uint32_t w0 = kw[hf][0][j], w1 = kw[hf][1][j], x0 = w0 >> 8, x1 = w1 >> 8;
+              const uint32_t a0[4] = {nib.lo(w0), nib.lo(w1), nib.hi(w0), nib.hi(w1)};
+              const uint32_t a1[4] = {nib.lo(x0), nib.lo(x1), nib.hi(x0), nib.hi(x1)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma(acc[hf][nt], a0, qf[nt][0], qf[nt][1], acc[hf][nt]);
+                mma(acc[hf][nt], a1, qf[nt][2], qf[nt][3], acc[hf][nt]);
+              }
+            }
+          }
+#pragma unroll
+          for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float sc = k < 2 ? s0[hf][g] : s1[hf][g];
+                S[hf][nt][k] = g == 0 ? sc * acc[hf][nt][k] : fmaf(sc, acc[hf][nt][k], S[hf][nt][k]);
+              }
+        }
+      }
+      // ---- logits against the reference; those outside a row's reach vanish. (A row that has seen nothing
+      // has ref -inf and e around 3e38 here, which raises its reference below.)
+      float top = NINF;
+      auto logits = [&] {
+        top = NINF;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float from = (float)P_SHIFT - fmaxf(ref[nt][k], -3.0e38f);
+            int2 seen = make_int2(0, 0);
+            if (EDGE) seen = reinterpret_cast<const int2*>(qs_seen)[nt * 8 + 2 * c + k];
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                float& x = e[hf][nt][k + 2 * u];
+                x = fmaf(S[hf][nt][k + 2 * u], fac[nt][k], from);
+                if (EDGE) {
+                  const int t = tk + 16 * hf + r + 8 * u;
+                  if (t >= seen.y || t < seen.x) x = NINF;
+                }
+                top = fmaxf(top, x);
+              }
+          }
+      };
+      logits();
+      if (__any_sync(0xffffffffu, top > 8.0f + P_SHIFT)) {  // raise the references to the largest logits so far
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float m = ref[nt][k];
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+              for (int u = 0; u < 4; u += 2)
+                if (e[hf][nt][k + u] != NINF) m = fmaxf(m, S[hf][nt][k + u] * fac[nt][k]);
+#pragma unroll
+            for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            const float f = ref[nt][k] == NINF ? 0.0f : ex2(ref[nt][k] - m);
+            ref[nt][k] = m;
+            sum[nt][k] *= f;
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+              ones[nt][q][k] *= f;
+              ones[nt][q][k + 2] *= f;
+            }
+#pragma unroll
+            for (int t = 0; t < 2 * J; ++t) {
+              o[nt][t][k] *= f;
+              o[nt][t][k + 2] *= f;
+            }
+          }
+        logits();
+      }
+      // ---- P 2^7 towards the MMA's B operand: [column][token]
+      uint32_t pb[HALVES][NT][2];
+#pragma unroll
+      for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            e[hf][nt][k] = ex2(e[hf][nt][k]);
+            sum[nt][k & 1] += e[hf][nt][k];
+          }
+          pb[hf][nt][0] = transpose8(pack_half(e[hf][nt][0], e[hf][nt][1]));
+          pb[hf][nt][1] = transpose8(pack_half(e[hf][nt][2], e[hf][nt][3]));
+        }
+      // ---- O^T
+#pragma unroll
+      for (int hf = 0; hf < HALVES; ++hf) {
+        const int sub = sub0 + hf;
+        uint32_t vs[2][NG];  // value scales of the token pairs 2c, 2c + 1 of both eights
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          lds<NG>(tile + 32 * D + 64 * NG + (8 * sub + 4 * hh + c) * (4 * NG), vs[hh]);
+          if (EDGE) {  // tokens outside the sequence hold whatever was there
+            const int t = tk + 16 * hf + 8 * hh + 2 * c;
+            const uint32_t keep = (t >= low && t < high ? 0xffffu : 0u) | (t + 1 >= low && t + 1 < high ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) vs[hh][g] &= keep;
+          }
+        }
+        uint32_t vw[2][J];  // [eight]: blocks by token b = 0, then b = 1
+        lds<J>(tile + 16 * D + sub * (8 * D) + (r * 4 + c) * (D / 8), vw[0]);
+        lds<J>(tile + 16 * D + sub * (8 * D) + 4 * D + (r * 4 + c) * (D / 8), vw[1]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          uint32_t pv[NT][2];
+          const uint32_t sv[2] = {mul_half2(vs[0][g], vdown), mul_half2(vs[1][g], vdown)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              pv[nt][hh] = mul_half2(pb[hf][nt][hh], sv[hh]);
+              if (EDGE) {
+                // An infinite or NaN scale makes the row's group NaN if the row sees the token, and only that:
+                // kept apart from the sums, which other groups and rows share an MMA with.
+                const uint32_t odd = odd_halves(vs[hh][g]), x = pb[hf][nt][hh];
+                if (odd & (((x & 0x7fffu) ? 0xffffu : 0u) | ((x & 0x7fff0000u) ? 0xffff0000u : 0u))) poison |= 1u << (nt * NG + g);
+                pv[nt][hh] &= ~odd;
+              }
+            }
+          constexpr uint32_t ONE = 0x3C003C00u;
+          const uint32_t one[4] = {g & 1 ? 0u : ONE, g & 1 ? ONE : 0u, g & 1 ? 0u : ONE, g & 1 ? ONE : 0u};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma(ones[nt][g / 2], one, pv[nt][0], pv[nt][1], ones[nt][g / 2]);
+#pragma unroll
+          for (int jj = 0; jj < JG; ++jj) {
+            const int j = g * JG + jj;
+            const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+            uint32_t xa = prmt(vw[0][j / 2], vw[0][J / 2 + j / 2], sel);
+            uint32_t xb = prmt(vw[1][j / 2], vw[1][J / 2 + j / 2], sel);
+            const uint32_t a0[4] = {nib.lo(xa), nib.hi(xa), nib.lo(xb), nib.hi(xb)};
+            xa >>= 8;
+            xb >>= 8;
+            const uint32_t a1[4] = {nib.lo(xa), nib.hi(xa), nib.lo(xb), nib.hi(xb)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma(o[nt][2 * j], a0, pv[nt][0], pv[nt][1], o[nt][2 * j]);
+              mma(o[nt][2 * j + 1], a1, pv[nt][0], pv[nt][1], o[nt][2 * j + 1]);
+            }
+          }
+        }
+      }
+    };
 
     for (int i = 0; i < count; ++i) {
       const int s = i % L::ST;
@@ -390,171 +638,58 @@ __global__ void __launch_bounds__(CTA) attention_kernel(const __grid_constant__ 
       have &= ~(1u << s);
       const uint32_t tile = ring + s * L::TILE;
       const int tok0 = (tile0 + i * W) * 32;
+      bool edge = tok0 < all_lo || tok0 + 32 > all_hi;
+      // ---- the tile's largest value scale (tokens outside the sequence do not count)
+      uint32_t big = 0;
+      auto largest = [&](bool drop) {  // drop: leave out infinities and NaN
+        big = 0;
+#pragma unroll
+        for (int w = 0; w < 16 * NG; w += 32) {
+          uint32_t x[1] = {0};
+          if (16 * NG >= 32 || lane < 16 * NG) lds<1>(tile + 32 * D + 64 * NG + (w + lane) * 4, x);
+          if (edge) {
+            const int t = tok0 + 2 * ((w + lane) / NG);
+            x[0] &= (t >= low && t < high ? 0xffffu : 0u) | (t + 1 >= low && t + 1 < high ? 0xffff0000u : 0u);
+          }
+          if (drop) x[0] &= ~odd_halves(x[0]);
+          big = max_half2_nan(big, x[0]);
+        }
+        const __half2 h = *reinterpret_cast<const __half2*>(&big);
+        return __half2float(__hmax_nan(__low2half(h), __high2half(h)));
+      };
+      float bm = largest(false);
+      if (__any_sync(0xffffffffu, !(bm <= __uint_as_float((uint32_t)(127 + vexp) << 23)))) {
+        if (__any_sync(0xffffffffu, !(bm <= 65504.0f))) {  // scales that stand for NaN: the careful path
+          bm = largest(true);
+          edge = true;
+        }
+#pragma unroll
+        for (int x = 1; x < 32; x *= 2) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
+        const int be = min(max((int)(__float_as_uint(bm) >> 23) - 126, -14), 16);  // bm <= 2^be
+        const int nexp = max(vexp, be);
+        const float down = __uint_as_float((uint32_t)(127 + vexp - nexp) << 23);
+        vexp = nexp;
+        vdown = (uint32_t)__half_as_ushort(__float2half_rn(__uint_as_float((uint32_t)(127 - vexp) << 23))) * 0x00010001u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int q = 0; q < NP; ++q) ones[nt][q][k] *= down;
+#pragma unroll
+            for (int t = 0; t < 2 * J; ++t) o[nt][t][k] *= down;
+          }
+      }
+      if (!edge) {
+        if constexpr (HALVES == 2) part(std::false_type{}, std::integral_constant<int, 2>{}, tile, 0, tok0);
+        else
 #pragma unroll 1
-      for (int sub = 0; sub < 2; ++sub) {
-        const int tk = tok0 + 16 * sub;
-        if (tk >= high || tk + 16 <= low) continue;
-        const bool edge = tk < all_lo || tk + 16 > all_hi;
-        // ---- S^T: tokens r, r + 8 by columns 2c, 2c + 1
-        float S[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) S[nt][k] = 0.0f;
-        uint32_t k0[J], k1[J];
-        lds<J>(tile + (16 * sub + r) * (D / 2) + c * (D / 8), k0);
-        lds<J>(tile + (16 * sub + r + 8) * (D / 2) + c * (D / 8), k1);
-        float s0[NG], s1[NG];
-        key_scales<NG>(tile + 32 * D + (16 * sub + r) * (2 * NG), s0);
-        key_scales<NG>(tile + 32 * D + (16 * sub + r + 8) * (2 * NG), s1);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float acc[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            acc[nt][0] = acc[nt][2] = bias[nt][g][0];
-            acc[nt][1] = acc[nt][3] = bias[nt][g][1];
-          }
-#pragma unroll
-          for (int jj = 0; jj < JG; ++jj) {
-            const int j = g * JG + jj;
-            const uint32_t a0[4] = {lo_nib(k0[j]), lo_nib(k1[j]), hi_nib(k0[j]), hi_nib(k1[j])};
-            const uint32_t x0 = k0[j] >> 8, x1 = k1[j] >> 8;
-            const uint32_t a1[4] = {lo_nib(x0), lo_nib(x1), hi_nib(x0), hi_nib(x1)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              uint32_t qf[4];
-              lds<4>(smem_u32(qs) + ((nt * J + j) * 32 + lane) * 16, qf);
-              mma(acc[nt], a0, qf[0], qf[1], acc[nt]);
-              mma(acc[nt], a1, qf[2], qf[3], acc[nt]);
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            S[nt][0] = fmaf(s0[g], acc[nt][0], S[nt][0]);
-            S[nt][1] = fmaf(s0[g], acc[nt][1], S[nt][1]);
-            S[nt][2] = fmaf(s1[g], acc[nt][2], S[nt][2]);
-            S[nt][3] = fmaf(s1[g], acc[nt][3], S[nt][3]);
-          }
-        }
-        // ---- value scales of the pairs c, c + 4 of this half tile
-        uint32_t vs[2][NG];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          lds<NG>(tile + 32 * D + 64 * NG + (8 * sub + 4 * hh + c) * (4 * NG), vs[hh]);
-          if (edge) {  // tokens outside the sequence hold whatever was there
-            const int t = tk + 8 * hh + 2 * c;
-            const uint32_t keep = (t >= low && t < high ? 0xffffu : 0u) | (t + 1 >= low && t + 1 < high ? 0xffff0000u : 0u);
-#pragma unroll
-            for (int g = 0; g < NG; ++g) vs[hh][g] &= keep;
-          }
-        }
-        uint32_t big = vs[0][0];
-#pragma unroll
-        for (int g = 0; g < NG; ++g) big = max_half2(big, max_half2(vs[0][g], vs[1][g]));
-        // ---- logits; those outside a row's reach vanish
-        float top = NINF;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            S[nt][k] *= fac[nt][k & 1];
-            if (edge) {
-              const int t = tk + r + 8 * (k >> 1);
-              if (t >= seen_hi[nt][k & 1] || t < seen_lo[nt][k & 1]) S[nt][k] = NINF;
-            }
-            top = fmaxf(top, S[nt][k] - ref[nt][k & 1]);
-          }
-        const __half2 big2 = *reinterpret_cast<const __half2*>(&big);
-        const float bigf = fmaxf(__low2float(big2), __high2float(big2));
-        const float vtop = __uint_as_float((uint32_t)(127 + vexp) << 23);
-        if (__any_sync(0xffffffffu, top > 8.0f || bigf > vtop)) {
-          // raise the references of all rows to their largest logit so far, and the values' exponent
-          float bm = bigf;
-#pragma unroll
-          for (int x = 1; x < 32; x *= 2) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
-          const int be = min(max((int)(__float_as_uint(bm) >> 23) - 126, -14), 16);  // bm <= 2^be
-          const int nexp = max(vexp, be);
-          const float down = __uint_as_float((uint32_t)(127 + vexp - nexp) << 23);
-          vexp = nexp;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float m = fmaxf(S[nt][k], S[nt][k + 2]);
-#pragma unroll
-              for (int x = 4; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-              m = fmaxf(m, ref[nt][k]);
-              const float f = ref[nt][k] == NINF ? 0.0f : ex2(ref[nt][k] - m);
-              ref[nt][k] = m;
-              sum[nt][k] *= f;
-              const float fo = f * down;
-#pragma unroll
-              for (int t = 0; t < 2 * J; ++t) {
-                o[nt][t][k] *= fo;
-                o[nt][t][k + 2] *= fo;
-              }
-#pragma unroll
-              for (int g = 0; g < NG; ++g) {
-                ones[nt][g][k] *= fo;
-                ones[nt][g][k + 2] *= fo;
-              }
-            }
-        }
-        // ---- P 2^7 towards the MMA's B operand: [column][token]
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float e[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // a row that has seen nothing yet has ref -inf: all its logits here are -inf too
-            const float at = fmaxf(ref[nt][k & 1], -3.0e38f);
-            e[k] = ex2(S[nt][k] - at + (float)P_SHIFT);
-            sum[nt][k & 1] += e[k];
-          }
-          pb[nt][0] = transpose8(pack_half(e[0], e[1]));
-          pb[nt][1] = transpose8(pack_half(e[2], e[3]));
-        }
-        const __half vdown1 = __float2half_rn(__uint_as_float((uint32_t)(127 - vexp) << 23));
-        const uint32_t vdown = (uint32_t)__half_as_ushort(vdown1) * 0x00010001u;
-        // ---- O^T
-        uint32_t vw[2][J];  // [h]: blocks by token b = 0, then b = 1
-        lds<J>(tile + 16 * D + sub * (8 * D) + (r * 4 + c) * (D / 8), vw[0]);
-        lds<J>(tile + 16 * D + sub * (8 * D) + 4 * D + (r * 4 + c) * (D / 8), vw[1]);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          uint32_t pv[NT][2];
-          const uint32_t sv[2] = {mul_half2(vs[0][g], vdown), mul_half2(vs[1][g], vdown)};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              pv[nt][hh] = mul_half2(pb[nt][hh], sv[hh]);
-              if (edge) {  // a NaN or infinite scale of a token that this row does not see
-                const uint32_t x = pb[nt][hh];
-                pv[nt][hh] &= ((x & 0x7fffu) ? 0xffffu : 0u) | ((x & 0x7fff0000u) ? 0xffff0000u : 0u);
-              }
-            }
-          const uint32_t one[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma(ones[nt][g], one, pv[nt][0], pv[nt][1], ones[nt][g]);
-#pragma unroll
-          for (int jj = 0; jj < JG; ++jj) {
-            const int j = g * JG + jj;
-            const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-            uint32_t xa = prmt(vw[0][j / 2], vw[0][J / 2 + j / 2], sel);
-            uint32_t xb = prmt(vw[1][j / 2], vw[1][J / 2 + j / 2], sel);
-            const uint32_t a0[4] = {lo_nib(xa), hi_nib(xa), lo_nib(xb), hi_nib(xb)};
-            xa >>= 8;
-            xb >>= 8;
-            const uint32_t a1[4] = {lo_nib(xa), hi_nib(xa), lo_nib(xb), hi_nib(xb)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma(o[nt][2 * j], a0, pv[nt][0], pv[nt][1], o[nt][2 * j]);
-              mma(o[nt][2 * j + 1], a1, pv[nt][0], pv[nt][1], o[nt][2 * j + 1]);
-            }
-          }
+          for (int sub = 0; sub < 2; ++sub) part(std::false_type{}, std::integral_constant<int, 1>{}, tile, sub, tok0 + 16 * sub);
+      } else {
+#pragma unroll 1
+        for (int sub = 0; sub < 2; ++sub) {
+          const int tk = tok0 + 16 * sub;
+          if (tk < high && tk + 16 > low) part(std::true_type{}, std::integral_constant<int, 1>{}, tile, sub, tk);
         }
       }
       __syncwarp();
@@ -564,6 +699,8 @@ __global__ void __launch_bounds__(CTA) attention_kernel(const __grid_constant__ 
     // ---- this warp's sums into shared memory (its ring is drained), then the CTA's join
     float* mine = reinterpret_cast<float*>(smem + warp * L::RING);
     const float back = __uint_as_float((uint32_t)(127 + vexp - P_SHIFT) << 23);
+    poison |= __shfl_xor_sync(0xffffffffu, poison, 1);
+    poison |= __shfl_xor_sync(0xffffffffu, poison, 2);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -576,12 +713,18 @@ __global__ void __launch_bounds__(CTA) attention_kernel(const __grid_constant__ 
           ml[(warp * L::ROWS + rr) * 2] = ref[nt][k];
           ml[(warp * L::ROWS + rr) * 2 + 1] = l * (1.0f / (1 << P_SHIFT));
         }
+        const uint32_t bad = __shfl_sync(0xffffffffu, poison, (2 * c + k) * 4) >> (nt * NG);
+        float off[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          off[g] = 8.0f * ones[nt][g / 2][k + 2 * (g & 1)];
+          if (bad >> g & 1) off[g] = __int_as_float(0x7fffffff);
+        }
 #pragma unroll
         for (int t = 0; t < 2 * J; ++t) {
-          const float off = 8.0f * ones[nt][t / 2 / JG][k];
           const int d = 32 * (t / 2) + 4 * r + 2 * (t & 1);
-          mine[rr * (D + 4) + d] = (o[nt][t][k] * 16777216.0f - off) * back;
-          mine[rr * (D + 4) + d + 1] = (o[nt][t][k + 2] * 1048576.0f - off) * back;
+          mine[rr * (D + 4) + d] = (o[nt][t][k] * 16777216.0f - off[t / 2 / JG]) * back;
+          mine[rr * (D + 4) + d + 1] = (o[nt][t][k + 2] * 1048576.0f - off[t / 2 / JG]) * back;
         }
       }
     __syncthreads();
@@ -625,40 +768,86 @@ __global__ void __launch_bounds__(CTA) attention_kernel(const __grid_constant__ 
   }
 }
 
-// Joins the parts of a row: one warp per (new token, query head).
-template <int D>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Params p) {
-  constexpr int V = D / 32;
+// Joins the parts of a row (new token, query head): WPR warps of it each take every WPR-th part, eight loads
+// in flight, and the first one finishes the row.
+constexpr int JOIN_CTA = 256;
+template <int D, int WPR>
+__global__ void __launch_bounds__(JOIN_CTA) join_kernel(const __grid_constant__ Params p) {
+  constexpr int V = D / 32, ROWS = JOIN_CTA / 32 / WPR;
+  __shared__ float parts[WPR > 1 ? WPR : 1][WPR > 1 ? D : 1];
+  __shared__ float sums[WPR];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= p.c.T * p.Hq) return;
-  if (kv4_seq_of(p.c, row / p.Hq) < 0) return;  // behind the last sequence: left as it was
-  const float* ml = p.part_ml + row * p.splits * 2;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) % WPR;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + (threadIdx.x >> 5) / WPR;
+  // (rows behind the last sequence are left as they were; with WPR > 1 a CTA has one row)
+  if (row >= p.c.T * p.Hq || kv4_seq_of(p.c, row / p.Hq) < 0) return;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row * p.splits;
   float m = NINF;
-  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, ml[2 * s]);
+  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, ml[s].x);
 #pragma unroll
   for (int x = 1; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   float l = 0.0f, o[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.0f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float ms = ml[2 * s], ls = ml[2 * s + 1];
-    if (ms == NINF && ls == 0.0f) continue;
-    const float f = ms == NINF ? 1.0f : ex2(ms - m);
-    l += ls * f;
-    const float* src = p.part + (row * p.splits + s) * D + lane * V;
+  const float* src = p.part + row * p.splits * D + lane * V;
+  constexpr int AHEAD = 8;
+  for (int s0 = w; s0 < p.splits; s0 += AHEAD * WPR) {
+    float x[AHEAD][V];
+    float2 t[AHEAD];
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = fmaf(src[i], f, o[i]);
+    for (int a = 0; a < AHEAD; ++a) {
+      const int s = s0 + a * WPR;
+      t[a] = make_float2(NINF, 0.0f);
+      if (s < p.splits) {
+        t[a] = ml[s];
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(src + (int64_t)s * D + i);
+          x[a][i] = y.x;
+          x[a][i + 1] = y.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      if (t[a].x == NINF && t[a].y == 0.0f) continue;  // a part that saw nothing
+      const float f = t[a].x == NINF ? 1.0f : ex2(t[a].x - m);  // (only NaN logits: kept)
+      l += t[a].y * f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = fmaf(x[a][i], f, o[i]);
+    }
+  }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) parts[w][lane * V + i] = o[i];
+    if (lane == 0) sums[w] = l;
+    __syncthreads();
+    if (w) return;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) {
+      l += sums[k];
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] += parts[k][lane * V + i];
+    }
   }
   finish_row<D>(p, o, l, row, lane);
 }
 
-template <class K>
-rot_status launch(K kernel, int64_t ctas, int threads, int smem, cudaStream_t s, const Params& p) {
+// KERNEL's shared memory is allowed once per device.
+template <auto KERNEL>
+rot_status launch(int64_t ctas, int threads, int smem, cudaStream_t s, const Params& p) {
   if (ctas > 0x7fffffff) return set_error(ROT_EUNSUPPORTED, "kv4_attention: too many rows for one launch");
-  if (smem > 48 * 1024) ROT_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  if (smem > 48 * 1024) {
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    ROT_CUDA_TRY(cudaGetDevice(&dev));
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!bit || !(allowed.load(std::memory_order_relaxed) & bit)) {
+      ROT_CUDA_TRY(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+      allowed.fetch_or(bit);
+    }
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(threads);
@@ -669,7 +858,7 @@ rot_status launch(K kernel, int64_t ctas, int threads, int smem, cudaStream_t s,
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = pdl_default() ? 1 : 0;
-  ROT_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, p));
+  ROT_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, p));
   return ROT_OK;
 }
 
@@ -677,10 +866,12 @@ template <int D, int NG, int NT>
 rot_status run(const Params& p, bool q_f32, cudaStream_t s) {
   const int64_t ctas = (int64_t)p.c.B * p.chunks * p.c.heads * p.splits;
   constexpr int smem = Lay<D, NG, NT>::SMEM;
-  rot_status st = q_f32 ? launch(attention_kernel<D, NG, NT, true>, ctas, CTA, smem, s, p)
-                        : launch(attention_kernel<D, NG, NT, false>, ctas, CTA, smem, s, p);
+  rot_status st = q_f32 ? launch<attention_kernel<D, NG, NT, true>>(ctas, CTA, smem, s, p)
+                        : launch<attention_kernel<D, NG, NT, false>>(ctas, CTA, smem, s, p);
   if (st || p.splits == 1) return st;
-  return launch(combine_kernel<D>, (p.c.T * p.Hq + 3) / 4, 128, 0, s, p);
+  // one warp walks up to 16 parts in two rounds of loads; more parts are spread over eight
+  return p.splits > 16 ? launch<join_kernel<D, 8>>(p.c.T * p.Hq, JOIN_CTA, 0, s, p)
+                       : launch<join_kernel<D, 1>>((p.c.T * p.Hq + 7) / 8, JOIN_CTA, 0, s, p);
 }
 
 template <int D, int NG>
@@ -699,11 +890,15 @@ Kv4Split kv4_split(int D, int B, int heads, int share, int window, int64_t max_n
   const int64_t rows = max_new * share;
   sp.rows = rows > 8 && D < 256 ? 16 : 8;
   sp.chunks = (int)std::min<int64_t>(std::max<int64_t>((rows + sp.rows - 1) / sp.rows, 1), 1 << 20);
+  // Parts of the length: as many CTAs as fit at once, with at least four tiles to a warp; up to three times
+  // as many, which evens out uneven lengths, where a warp keeps sixteen tiles. (A CTA's own start and end
+  // cost as much as about three of a warp's tiles.)
   const int64_t units = std::max<int64_t>((int64_t)B * heads * sp.chunks, 1);
-  const int64_t tiles = (max_len + KV4_TILE - 1) / KV4_TILE;
-  const int64_t want = (8 * (int64_t)sms + units - 1) / units;   // CTAs that fill the GPU a few times over
-  const int64_t most = (tiles + 4 * W - 1) / (4 * W);            // at least four tiles to a warp
-  sp.splits = (int)std::min<int64_t>(std::max<int64_t>(std::min(want, most), 1), 256);
+  const int64_t tiles = (max_len + KV4_TILE - 1) / KV4_TILE, at_once = 4 * (int64_t)sms;
+  const int64_t fit = std::min(at_once / units, (tiles + 4 * W - 1) / (4 * W));
+  const int64_t even = std::min((3 * at_once + units - 1) / units, tiles / (16 * W));
+  const int64_t want = std::max(fit, even), most = 256;
+  sp.splits = (int)std::min(std::max<int64_t>(want, 1), most);
   return sp;
 }
 
