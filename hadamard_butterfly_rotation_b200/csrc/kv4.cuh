@@ -65,11 +65,12 @@ __host__ __device__ inline int kv4_seq_of(const Kv4View& c, int64_t t) {
 // Byte offset of head h's tile `tile` (token >> 5) of sequence b, or -1 where the table has no such
 // page or names one outside the cache: nothing is read or written there.
 __host__ __device__ inline int64_t kv4_tile_at(const Kv4View& c, int b, int64_t tile, int h) {
-  const int64_t slot = tile / c.tpp;
-  if (tile < 0 || slot >= c.table_pages) return -1;
+  if (tile < 0) return -1;
+  const uint32_t slot = (uint32_t)tile / (uint32_t)c.tpp;  // (lengths are below 2^31)
+  if (slot >= (uint32_t)c.table_pages) return -1;
   const int64_t page = c.table[(int64_t)b * c.table_stride + slot];
   if (page < 0 || page >= c.pages) return -1;
-  return page * c.page_stride + ((int64_t)h * c.tpp + (tile - slot * c.tpp)) * c.tile_bytes;
+  return page * c.page_stride + (int64_t)(h * c.tpp + (int)((uint32_t)tile - slot * (uint32_t)c.tpp)) * c.tile_bytes;
 }
 
 // Where packed row `row` of head h lies: its sequence (-1 behind the last one), its position and its
@@ -96,23 +97,34 @@ __device__ __forceinline__ float kv4_signed(float v, uint32_t word, int hi) {
 }
 
 // Unnormalised Walsh-Hadamard transform of rows spread over `LANES` neighbouring lanes, V coordinates
-// each: the lowest log2 V stages in registers, the others by shuffles.
+// each: the lowest log2 V stages in registers, the others by shuffles; two values to an addition.
 template <int V, int LANES>
 __device__ __forceinline__ void kv4_fwht(float (&v)[V], int lane) {
 #pragma unroll
-  for (int s = 1; s < V; s *= 2)
+  for (int i = 0; i < V; i += 2) {
+    const float a = v[i], b = v[i + 1];
+    v[i] = a + b;
+    v[i + 1] = a - b;
+  }
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!(i & s)) {
-        const float a = v[i], b = v[i + s];
-        v[i] = a + b;
-        v[i + s] = a - b;
-      }
+  for (int s = 2; s < V; s *= 2)
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+      if (!(i & s)) bfly_x2(v[i], v[i + 1], v[i + s], v[i + s + 1]);
 #pragma unroll
   for (int m = 1; m < LANES; m *= 2) {
     const float sg = (lane & m) ? -1.0f : 1.0f;
+    unsigned long long sg2;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(sg2) : "f"(sg));
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = fmaf(v[i], sg, __shfl_xor_sync(0xffffffffu, v[i], m));
+    for (int i = 0; i < V; i += 2) {
+      const float x = __shfl_xor_sync(0xffffffffu, v[i], m), y = __shfl_xor_sync(0xffffffffu, v[i + 1], m);
+      unsigned long long a, b, d;
+      asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(v[i]), "f"(v[i + 1]));
+      asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(x), "f"(y));
+      asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(sg2), "l"(b));
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(v[i]), "=f"(v[i + 1]) : "l"(d));
+    }
   }
 }
 

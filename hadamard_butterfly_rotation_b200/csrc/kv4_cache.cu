@@ -1,10 +1,11 @@
 // Writing the paged 4-bit key/value cache (rotate, quantise, pack, place) and reading it back.
 //
-// One row (a token's key or value of one head) is D/32 lanes of 32 coordinates: a lane holds block j of
-// the tile layout (kv4.cuh), so a quantisation group of 32 needs no shuffle, the lowest five stages of
-// the Walsh-Hadamard transform run in registers, and the rest are one shuffle per value and stage.
-// A warp takes 1024/D consecutive tokens of one head, so that the pieces of eight neighbouring tokens
-// which the value layout interleaves leave in one store instruction.
+// A row is a token's key or value of one head; four lanes l share it and own the coordinates
+// 32 j + 8 l + i, i < 8, of every block j: those of piece c = l of a key in the tile layout (kv4.cuh), of the
+// pieces r = 2 l and 2 l + 1 of a value. So a lane's codes are one contiguous piece of the tile, or two, its
+// 16-bit coordinates are 16-byte pieces that the four lanes continue to 64, and no code changes lanes. The
+// Walsh-Hadamard stages over i and j run in registers, those over l are two rounds of shuffles. A warp takes
+// eight rows at a time and fetches the next eight while it works on these.
 // Both kernels are bound by HBM traffic (rows in or out at full width, codes at 4 bits).
 #include "kv4.cuh"
 
@@ -13,65 +14,167 @@ namespace {
 
 __device__ int g_kv4_cache_error = 0;
 
-constexpr int CTA = 128;
+constexpr int CTA = 128;  // two warps for keys, two for values
+// CTAs that an SM holds, by the registers that are left to a thread: appending 12.9 k tokens of 8 x 128 took
+// 22 us with 4 (128 registers), 25 us with 5 and 29 us with 6, reading 72 k of them 96, 89 and 86 us.
+constexpr int append_ctas(int D) { return D == 256 ? 2 : 4; }
+constexpr int read_ctas(int D) { return D == 256 ? 2 : 6; }
 
-// 32 coordinates from global memory as fp32
-template <bool F32>
-__device__ __forceinline__ void load32(const void* base, int64_t at, float (&v)[32]) {
-  if constexpr (F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+// A lane's coordinates of a row: value x of N is coordinate 32 (x / 8) + 8 l + x % 8.
+constexpr int LANES = 4;
+__device__ __forceinline__ int coordinate(int l, int x) { return 32 * (x / 8) + 8 * l + x % 8; }
+
+// ... as they stand in memory: W words to the block of eight
+template <int D, bool F32>
+struct Raw {
+  static constexpr int W = F32 ? 8 : 4;
+  uint32_t w[D / 32][W];
+  __device__ __forceinline__ void load(const void* base, int64_t at, int l) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 x = __ldg(p + i);
-      v[4 * i] = x.x;
-      v[4 * i + 1] = x.y;
-      v[4 * i + 2] = x.z;
-      v[4 * i + 3] = x.w;
-    }
-  } else {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
+    for (int j = 0; j < D / 32; ++j) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + (at + 32 * j + 8 * l) * (W / 2));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 x = __ldg(p + i);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
-        v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      for (int i = 0; i < W; i += 4) {
+        const uint4 x = __ldg(p + i / 4);
+        w[j][i] = x.x;
+        w[j][i + 1] = x.y;
+        w[j][i + 2] = x.z;
+        w[j][i + 3] = x.w;
       }
     }
   }
-}
-
-template <bool F32>
-__device__ __forceinline__ void store32(void* base, int64_t at, const float (&v)[32]) {
-  if constexpr (F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+  __device__ __forceinline__ void store(void* base, int64_t at, int l) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  } else {
-    uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at);
+    for (int j = 0; j < D / 32; ++j) {
+      uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + (at + 32 * j + 8 * l) * (W / 2));
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      p[i] = make_uint4(kv4_pack_bf16(v[8 * i], v[8 * i + 1]), kv4_pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                        kv4_pack_bf16(v[8 * i + 4], v[8 * i + 5]), kv4_pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+      for (int i = 0; i < W; i += 4) p[i / 4] = make_uint4(w[j][i], w[j][i + 1], w[j][i + 2], w[j][i + 3]);
+    }
   }
-}
-
-__device__ __forceinline__ void apply_signs(float (&v)[32], const uint32_t* sign, int j) {
+  // Signs from the plan's mask, whose word p has those of coordinates 2 p (bit 15) and 2 p + 1 (bit 31). Read
+  // anew for every row: the lines stay in L1, and sixteen registers do not stay taken.
+  __device__ __forceinline__ void flip(const uint32_t* signs, int l) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t w = __ldg(sign + 16 * j + i);
-    v[2 * i] = kv4_signed(v[2 * i], w, 0);
-    v[2 * i + 1] = kv4_signed(v[2 * i + 1], w, 1);
+    for (int j = 0; j < D / 32; ++j) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(signs + 16 * j + 4 * l));
+      const uint32_t sign[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (F32) {
+          w[j][2 * i] ^= (sign[i] << 16) & 0x80000000u;
+          w[j][2 * i + 1] ^= sign[i] & 0x80000000u;
+        } else {
+          w[j][i] ^= sign[i] & 0x80008000u;
+        }
+      }
+    }
   }
+  __device__ __forceinline__ void to_float(float (&v)[D / 4]) const {
+#pragma unroll
+    for (int x = 0; x < D / 4; ++x) {
+      if constexpr (F32) v[x] = __uint_as_float(w[x / 8][x % 8]);
+      else v[x] = __uint_as_float(x % 2 ? w[x / 8][x % 8 / 2] & 0xffff0000u : w[x / 8][x % 8 / 2] << 16);
+    }
+  }
+  __device__ __forceinline__ void from_float(const float (&v)[D / 4]) {
+#pragma unroll
+    for (int x = 0; x < D / 4; x += 2) {
+      if constexpr (F32) {
+        w[x / 8][x % 8] = __float_as_uint(v[x]);
+        w[x / 8][x % 8 + 1] = __float_as_uint(v[x + 1]);
+      } else {
+        w[x / 8][x % 8 / 2] = kv4_pack_bf16(v[x], v[x + 1]);
+      }
+    }
+  }
+};
+
+// The lane's codes of token t in its tile, word j block j's eight: a key has them in one piece of D / 8 bytes,
+// a value in two of D / 16 whose halfwords are block j's lower and upper four.
+template <int D>
+struct Codes {
+  static constexpr int J = D / 32;
+  uint32_t w[J];
+  static __device__ __forceinline__ int key_at(int t, int l) { return t * (D / 2) + l * (D / 8); }
+  static __device__ __forceinline__ int value_at(int t, int l) {
+    return 16 * D + (t >> 3) * (4 * D) + 2 * l * (D / 2) + ((t & 7) >> 1) * (D / 8) + (t & 1) * (D / 16);
+  }
+  template <int N>
+  static __device__ __forceinline__ void get(const uint8_t* from, uint32_t* to) {
+    if constexpr (N == 1) to[0] = *reinterpret_cast<const uint32_t*>(from);
+    else if constexpr (N == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(from);
+      to[0] = x.x;
+      to[1] = x.y;
+    } else
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(from + 4 * i);
+        to[i] = x.x;
+        to[i + 1] = x.y;
+        to[i + 2] = x.z;
+        to[i + 3] = x.w;
+      }
+  }
+  template <int N>
+  static __device__ __forceinline__ void put(uint8_t* to, const uint32_t* w) {
+    if constexpr (N == 1) *reinterpret_cast<uint32_t*>(to) = w[0];
+    else if constexpr (N == 2) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+    else
+#pragma unroll
+      for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(to + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
+  // As read: a value's two pieces still apart (words 0 .. J/2 - 1 the lower fours)
+  __device__ __forceinline__ void load(const uint8_t* tile, int t, int l, bool val) {
+    if (!val) {
+      get<J>(tile + key_at(t, l), w);
+    } else {
+      get<J / 2>(tile + value_at(t, l), w);
+      get<J / 2>(tile + value_at(t, l) + D / 2, w + J / 2);
+    }
+  }
+  __device__ __forceinline__ void join(bool val) {
+    if (!val) return;
+    uint32_t v[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) v[j] = prmt(w[j / 2], w[J / 2 + j / 2], j & 1 ? 0x7632 : 0x5410);
+#pragma unroll
+    for (int j = 0; j < J; ++j) w[j] = v[j];
+  }
+  __device__ __forceinline__ void store(uint8_t* tile, int t, int l, bool val) const {
+    if (!val) {
+      put<J>(tile + key_at(t, l), w);
+    } else {
+      uint32_t v[J];
+#pragma unroll
+      for (int k = 0; k < J / 2; ++k) {
+        v[k] = prmt(w[2 * k], w[2 * k + 1], 0x5410);
+        v[J / 2 + k] = prmt(w[2 * k], w[2 * k + 1], 0x7632);
+      }
+      put<J / 2>(tile + value_at(t, l), v);
+      put<J / 2>(tile + value_at(t, l) + D / 2, v + J / 2);
+    }
+  }
+};
+
+// Byte offset in its tile of the scale of group g of token t
+template <int D, int NG>
+__device__ __forceinline__ int scale_at(int t, int g, bool val) {
+  return val ? 32 * D + 64 * NG + ((t >> 1) * NG + g) * 4 + (t & 1) * 2 : 32 * D + (t * NG + g) * 2;
 }
 
-// A row's place; a page outside the cache is an error of the call's data.
-__device__ __forceinline__ Kv4Slot find(const Kv4View& c, int64_t row, int h) {
-  const Kv4Slot p = kv4_slot_of(c, row, h);
+// The places of a CTA's eight tokens, found once for all heads.
+struct Places {
+  int64_t at[8];  // byte offset of head 0's tile, or -1
+  int t[8];       // token in the tile, or -1 behind the last sequence
+};
+__device__ __forceinline__ void find(const Kv4View& c, int64_t row0, Places& places) {
+  if (threadIdx.x >= 8) return;
+  const Kv4Slot p = kv4_slot_of(c, row0 + threadIdx.x, 0);
+  // a page outside the cache is an error of the call's data
   if (p.pos >= 0 && p.at < 0) atomicExch(&g_kv4_cache_error, (int)ROT_EINVAL);
-  return p;
+  places.at[threadIdx.x] = p.at;
+  places.t[threadIdx.x] = p.seq < 0 ? -1 : (int)(p.pos & 31);
 }
 
 // Coordinate d of T x for the row at `base`, in 64 bits, by the whole warp.
@@ -101,225 +204,283 @@ __device__ __forceinline__ uint32_t decide(float y, float s) {
   return (uint32_t)(8 + (int)copysignf(q, v));
 }
 
-// Symmetric absmax int4 codes of the lane's 32 coordinates z (unnormalised where rotated, y = z norm):
+// Symmetric absmax int4 codes of the lane's coordinates z of a row (unnormalised where rotated, y = z norm):
 // s = binary16(fp32(max|y| / 7)), q = clamp(round_half_away(fp32(y / s))), decided as if the rotation had
 // been done in 64 bits and rounded once to fp32. The fp32 butterfly is off by some 3e-7 of the row's
 // largest value, so a decision that stands further than that from its border is taken as it is; the few
-// others (codes within 4e-6 of a half, about 8e-6 of them, and scales within 4e-7 of a binary16 midpoint,
+// others (codes within 5e-6 of a half, about 1e-5 of them, and scales within 4e-7 of a binary16 midpoint,
 // about 1e-3; more where the row's largest value is far above the group's) are taken again from a 64-bit
 // sum of their own, by the whole warp. A code that flips moves its value by a whole step, which no
 // tolerance on the value can tell from a mistake. A group that holds a NaN, or whose scale overflows,
-// keeps that scale and codes of 0. All lanes of the warp enter.
+// keeps that scale and codes of 0. Lane l of a row works out the scales of the groups g = l mod LANES and
+// returns them in scale[g / LANES]; w: the codes, block by block. All lanes of the warp enter.
 template <int D, int NG, bool F32>
-__device__ __forceinline__ void quantise(const float (&z)[32], bool rot, float norm, const void* base, int64_t at,
-                                         const uint32_t* sign, int lane, uint32_t (&w)[4], uint16_t* scale) {
-  constexpr int J = D / 32, L = J / NG;  // lanes of a row, of a group
-  const int j = lane % J;
-  float m = fabsf(z[0]);
-#pragma unroll
-  for (int i = 1; i < 32; ++i) m = kv4_max_nan(m, fabsf(z[i]));
-#pragma unroll
-  for (int x = 1; x < L; x *= 2) m = kv4_max_nan(m, __shfl_xor_sync(0xffffffffu, m, x));
-  float row = m;
-#pragma unroll
-  for (int x = L; x < J; x *= 2) row = fmaxf(row, __shfl_xor_sync(0xffffffffu, row, x));
+__device__ __forceinline__ void quantise(const float (&z)[D / 4], bool rot, float norm, const void* base, int64_t at,
+                                         const uint32_t* sign, int lane, uint32_t (&w)[D / 32],
+                                         uint16_t (&scale)[(NG + LANES - 1) / LANES]) {
+  constexpr int N = D / 4;
+  constexpr int M = N / NG;                                 // the lane's coordinates of a group
+  constexpr int OWN = (NG + LANES - 1) / LANES;          // groups whose scales the lane works out
+  const int l = lane % LANES;
   const float n1 = rot ? norm : 1.0f;
-  float q7 = __fdiv_rn(m * n1, 7.0f);
-  // the row's largest value over the group's; without a rotation z is exact, only the quotient is not
-  const float far = m > 0.0f ? (rot ? fminf(row / m, 1e6f) : 1.0f) : 0.0f;
-  auto candidates = [&](uint32_t mask, auto&& take) {  // exact values of the marked coordinates of every lane
+  float m[NG], row = 0.0f;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    m[g] = fabsf(z[g * M]);
+#pragma unroll
+    for (int i = 1; i < M; ++i) m[g] = kv4_max_nan(m[g], fabsf(z[g * M + i]));
+#pragma unroll
+    for (int x = 1; x < LANES; x *= 2) m[g] = kv4_max_nan(m[g], __shfl_xor_sync(0xffffffffu, m[g], x));
+    row = fmaxf(row, m[g]);
+  }
+  // exact values of the marked coordinates (of 32 from x0 on) of every lane
+  auto candidates = [&](uint32_t mask, int x0, auto&& take) {
     uint32_t left;
     while ((left = __ballot_sync(0xffffffffu, mask != 0))) {
       const int src = __ffs(left) - 1;
       const int i = __shfl_sync(0xffffffffu, __ffs(mask) - 1, src);
-      const double y = exact_coordinate<D, F32>(base, __shfl_sync(0xffffffffu, at, src), sign, 32 * (src % J) + i, lane);
+      const double y = exact_coordinate<D, F32>(base, __shfl_sync(0xffffffffu, at, src), sign,
+                                                coordinate(src % LANES, x0 + i), lane);
       if (lane == src) {
         mask &= mask - 1;
         take(i, y);
       }
     }
   };
-  if (rot) {
-    const float eps = 4e-7f * far;
-    const bool near = __half_as_ushort(__float2half_rn(q7 * (1.0f - eps))) != __half_as_ushort(__float2half_rn(q7 * (1.0f + eps)));
-    if (__any_sync(0xffffffffu, near)) {
-      uint32_t mask = 0;
-      if (near)
+  // ---- scales
+  float q7[OWN], far[OWN];
+  bool near = false;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) mask |= (fabsf(z[i]) >= m * (1.0f - 2.0f * eps) ? 1u : 0u) << i;
+  for (int k = 0; k < OWN; ++k) {
+    float mine = m[0];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+      if (g / LANES == k && l == g % LANES) mine = m[g];
+    // the row's largest value over the group's; without a rotation z is exact, only the quotient is not
+    far[k] = mine > 0.0f ? (rot ? fminf(__fdividef(row, mine), 1e6f) : 1.0f) : 0.0f;
+    q7[k] = __fdiv_rn(mine * n1, 7.0f);
+    const float eps = 4e-7f * far[k];
+    near |= __half_as_ushort(__float2half_rn(q7[k] * (1.0f - eps))) != __half_as_ushort(__float2half_rn(q7[k] * (1.0f + eps)));
+  }
+  if (rot && __any_sync(0xffffffffu, near)) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const bool own = l == g % LANES;
+      const float eps = 4e-7f * far[g / LANES], q = q7[g / LANES];
+      const bool mine = own && __half_as_ushort(__float2half_rn(q * (1.0f - eps))) != __half_as_ushort(__float2half_rn(q * (1.0f + eps)));
+      // (a row's owner lane of the group tells the row's other lanes)
+      const int src = lane / LANES * LANES + g % LANES;
+      const bool hit = __shfl_sync(0xffffffffu, (int)mine, src);
+      const float least = m[g] * (1.0f - 2.0f * __shfl_sync(0xffffffffu, eps, src));
+      if (!__any_sync(0xffffffffu, hit)) continue;
       double big = 0.0;
-      candidates(mask, [&](int, double y) { big = fmax(big, fabs(y)); });
 #pragma unroll
-      for (int x = 1; x < L; x *= 2) big = fmax(big, __shfl_xor_sync(0xffffffffu, big, x));
-      if (near) q7 = __fdiv_rn((float)big, 7.0f);
-    }
-  }
-  const __half s16 = __float2half_rn(q7);
-  const uint32_t hb = __half_as_ushort(s16);
-  const float s = __half2float(s16);
-  *scale = (uint16_t)hb;
-  const bool ok = s > 0.0f && s <= 65504.0f;
-  const float f = ok ? __fdiv_rn(n1, s) : 0.0f;
-  constexpr float magic = magic_of_bits(4);
-  uint32_t u[32];
-  float worst = 0.0f;  // distance from the rounded code: a half is the border
+      for (int h = 0; h < M; h += 32) {
+        uint32_t mask = 0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    float t = __fmaf_rn(z[i], f, magic);
-    worst = fmaxf(worst, fabsf(__fmaf_rn(z[i], f, magic - t)));
-    u[i] = __float_as_uint(t);
-  }
-  if (((hb & 0x7fffu) - 0x0400u) >= 0x7800u) {  // zero, subnormal (|y / s| may pass 7.5), infinite or NaN scale
-#pragma unroll
-    for (int i = 0; i < 32; ++i) u[i] = ok ? code_magic_clamped(z[i], f, 7.0f, magic) : 8u;
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    w[k] = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[k] |= (u[8 * k + i] & 15u) << (4 * i);
-  }
-  const float border = 0.5f - 4e-6f * far;
-  const bool near = ok && worst >= border;
-  if (__any_sync(0xffffffffu, near)) {
-    uint32_t mask = 0;
-    if (near)
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float t = __fmaf_rn(z[i], f, magic);
-        mask |= (fabsf(__fmaf_rn(z[i], f, magic - t)) >= border ? 1u : 0u) << i;
+        for (int i = 0; i < (M < 32 ? M : 32); ++i) mask |= (hit && fabsf(z[g * M + h + i]) >= least ? 1u : 0u) << i;
+        candidates(mask, g * M + h, [&](int, double y) { big = fmax(big, fabs(y)); });
       }
-    auto patch = [&](int i, uint32_t code) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i / 8 == k) w[k] = (w[k] & ~(15u << (4 * (i & 7)))) | (code << (4 * (i & 7)));
-    };
-    if (rot) {
-      candidates(mask, [&](int i, double y) { patch(i, decide((float)y, s)); });
-    } else {
+      for (int x = 1; x < LANES; x *= 2) big = fmax(big, __shfl_xor_sync(0xffffffffu, big, x));
+      if (mine) q7[g / LANES] = __fdiv_rn((float)big, 7.0f);
+    }
+  }
+  float f[OWN], border[OWN];
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (mask >> i & 1) patch(i, decide(z[i], s));
+  for (int k = 0; k < OWN; ++k) {
+    const __half s16 = __float2half_rn(q7[k]);
+    const float s = __half2float(s16);
+    scale[k] = __half_as_ushort(s16);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    const bool normal = ((scale[k] & 0x7fffu) - 0x0400u) < 0x7800u;
+    f[k] = s > 0.0f && s <= 65504.0f ? r * n1 : 0.0f;
+    // the quotient is within 2e-6 of y / s; a subnormal scale (where |y / s| may pass 7.5) always looks twice
+    border[k] = normal ? 0.5f - 5e-6f * far[k] : f[k] > 0.0f ? -1.0f : 2.0f;
+  }
+  // ---- codes, 8 + q in the low bits of a sum with 2^23 + 8
+  constexpr float magic = magic_of_bits(4);
+  bool again = false;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const int src = lane / LANES * LANES + g % LANES;
+    const float fg = __shfl_sync(0xffffffffu, f[g / LANES], src), bg = __shfl_sync(0xffffffffu, border[g / LANES], src);
+    float worst = 0.0f;  // distance from the rounded code: a half is the border
+#pragma unroll
+    for (int x = g * M; x < (g + 1) * M; x += (M < 8 ? M : 8)) {
+      uint32_t pair[M < 8 ? M / 2 : 4];
+#pragma unroll
+      for (int i = 0; i < (M < 8 ? M : 8); i += 2) {
+        const float a = z[x + i], b = z[x + i + 1];
+        const float ta = __fmaf_rn(a, fg, magic), tb = __fmaf_rn(b, fg, magic);
+        worst = fmaxf(worst, fmaxf(fabsf(__fmaf_rn(a, fg, magic - ta)), fabsf(__fmaf_rn(b, fg, magic - tb))));
+        pair[i / 2] = __float_as_uint(tb) * 16u + __float_as_uint(ta);
+      }
+      if constexpr (M >= 8) {
+        w[x / 8] = prmt(prmt(pair[0], pair[1], 0x0040), prmt(pair[2], pair[3], 0x0040), 0x5410);
+        if (bg > 1.0f) w[x / 8] = 0x88888888u;  // no usable scale: codes of 0, whatever an infinity or NaN gave
+      } else {
+        const uint32_t half = bg > 1.0f ? 0x8888u : prmt(pair[0], pair[1], 0x0040);
+        w[x / 8] = x % 8 ? prmt(w[x / 8], half, 0x5410) : half;
+      }
+    }
+    again |= worst >= bg;
+  }
+  if (__any_sync(0xffffffffu, again)) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int src = lane / LANES * LANES + g % LANES;
+      const float fg = __shfl_sync(0xffffffffu, f[g / LANES], src), bg = __shfl_sync(0xffffffffu, border[g / LANES], src);
+      const float s = __half2float(__ushort_as_half((uint16_t)__shfl_sync(0xffffffffu, (int)scale[g / LANES], src)));
+#pragma unroll
+      for (int h = 0; h < M; h += 32) {
+        uint32_t mask = 0;
+#pragma unroll
+        for (int i = 0; i < (M < 32 ? M : 32); ++i) {
+          const float y = z[g * M + h + i], t = __fmaf_rn(y, fg, magic);
+          mask |= (fabsf(__fmaf_rn(y, fg, magic - t)) >= bg ? 1u : 0u) << i;
+        }
+        auto patch = [&](int x, uint32_t code) {
+#pragma unroll
+          for (int k = 0; k < N / 8; ++k)
+            if (x / 8 == k) w[k] = (w[k] & ~(15u << (4 * (x & 7)))) | (code << (4 * (x & 7)));
+        };
+        if (rot) {
+          candidates(mask, g * M + h, [&](int i, double y) { patch(g * M + h + i, decide((float)y, s)); });
+        } else {
+#pragma unroll
+          for (int i = 0; i < (M < 32 ? M : 32); ++i)
+            if (mask >> i & 1) patch(g * M + h + i, decide(z[g * M + h + i], s));
+        }
+      }
     }
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] ^= offset_xor_of_bits(4);
+  for (int k = 0; k < N / 8; ++k) w[k] ^= offset_xor_of_bits(4);
 }
 
+// A CTA takes eight tokens of `span` heads from h0 on: two of its warps go round the heads' keys, two round
+// their values.
 template <int D, int NG, bool F32>
-__global__ void __launch_bounds__(CTA) append_kernel(const Kv4View c, const Kv4Rows in, float norm, int64_t warps) {
-  constexpr int J = D / 32, TPW = 32 / J;
+__global__ void __launch_bounds__(CTA, append_ctas(D)) append_kernel(const __grid_constant__ Kv4View c,
+                                                                         const __grid_constant__ Kv4Rows in, float norm,
+                                                                         int span) {
+  __shared__ Places places;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31, j = lane % J;
-  const int64_t wid = (int64_t)blockIdx.x * (CTA / 32) + (threadIdx.x >> 5);
-  if (wid >= warps) return;
-  // warps: heads fastest, then keys / values, then token groups
-  const int h = (int)(wid % c.heads);
-  const int64_t rest = wid / c.heads;
-  const bool val = rest & 1;
-  const int64_t row = (rest >> 1) * TPW + lane / J;
+  const int64_t row0 = (int64_t)blockIdx.x * 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES, i = lane / LANES;
+  const int h0 = blockIdx.y * span, heads = min(span, c.heads - h0);
+  const bool val = warp >= 2, rot = val ? c.v_rot : c.k_rot;
+  const int64_t row = row0 + i, head = val ? in.v_head : in.k_head;
   const void* base = val ? in.v : in.k;
   // (lanes behind the last row take row 0's inputs, and store nothing)
-  const int64_t at = (row < c.T ? row : 0) * (val ? in.v_token : in.k_token) + h * (val ? in.v_head : in.k_head);
-  float z[32];
-  load32<F32>(base, at + 32 * j, z);
-  const Kv4Slot p = find(c, row, h);
-  const int t = (int)(p.pos & 31);
-  const bool rot = val ? c.v_rot : c.k_rot;
-  const uint32_t* sign = val ? c.v_sign : c.k_sign;
-  if (rot) {
-    if (sign) apply_signs(z, sign, j);
-    kv4_fwht<32, J>(z, lane);
-  }
-  uint32_t w[4];
-  uint16_t sc;
-  quantise<D, NG, F32>(z, rot, norm, base, at, sign, lane, w, &sc);
-  // values: lanes j and j ^ 1 swap halves of their words, so that each holds four words of two blocks
-  uint32_t o[4];
-  if (val) {
+  int64_t at = (row < c.T ? row : 0) * (val ? in.v_token : in.k_token) + (h0 + (warp & 1)) * head;
+  Raw<D, F32> raw;
+  if ((warp & 1) < heads) raw.load(base, at, l);
+  const uint32_t* signs = val ? c.v_sign : c.k_sign;
+  find(c, row0, places);
+  __syncthreads();
+  const int64_t tile = places.at[i];
+  const int t = places.t[i];
+#pragma unroll 1
+  for (int h = warp & 1; h < heads; h += 2) {
+    float z[D / 4];
+    if (rot && signs) raw.flip(signs, l);
+    raw.to_float(z);
+    const int64_t here = at;
+    at += 2 * head;
+    if (h + 2 < heads) raw.load(base, at, l);
+    if (rot) kv4_fwht<D / 4, LANES>(z, lane);
+    Codes<D> codes;
+    uint16_t scale[(NG + LANES - 1) / LANES];
+    quantise<D, NG, F32>(z, rot, norm, base, here, signs, lane, codes.w, scale);
+    if (tile >= 0) {
+      uint8_t* to = c.data + tile + (int64_t)(h0 + h) * c.tpp * c.tile_bytes;
+      codes.store(to, t, l, val);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      // word k: pieces r = 2k (low half) and 2k + 1 (high half); the even lane collects r = 2k
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, w[k], 1);
-      o[k] = (j & 1) ? prmt(other, w[k], 0x7632) : prmt(w[k], other, 0x5410);
+      for (int g = 0; g < NG; ++g)
+        if (l == g % LANES) *reinterpret_cast<uint16_t*>(to + scale_at<D, NG>(t, g, val)) = scale[g / LANES];
     }
-  }
-  if (p.at < 0) return;
-  uint8_t* tile = c.data + p.at;
-  if (!val) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      *reinterpret_cast<uint32_t*>(tile + t * (D / 2) + k * (D / 8) + j * 4) = w[k];
-    if (j % (J / NG) == 0)
-      *reinterpret_cast<uint16_t*>(tile + 32 * D + (t * NG + j / (J / NG)) * 2) = sc;
-  } else {
-    uint8_t* v = tile + 16 * D + (t >> 3) * (4 * D) + ((t & 7) >> 1) * (D / 8) + (t & 1) * (D / 16) + (j >> 1) * 4;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t*>(v + (2 * k + (j & 1)) * (D / 2)) = o[k];
-    if (j % (J / NG) == 0)
-      *reinterpret_cast<uint16_t*>(tile + 32 * D + 64 * NG + ((t >> 1) * NG + j / (J / NG)) * 4 + (t & 1) * 2) = sc;
   }
 }
 
 template <int D, int NG, bool F32>
-__global__ void __launch_bounds__(CTA) read_kernel(const Kv4View c, const Kv4Rows out, float norm, int inverse,
-                                                   int64_t warps) {
-  constexpr int J = D / 32, TPW = 32 / J;
+__global__ void __launch_bounds__(CTA, read_ctas(D)) read_kernel(const __grid_constant__ Kv4View c,
+                                                                       const __grid_constant__ Kv4Rows out, float norm,
+                                                                       int span, int inverse) {
+  __shared__ Places places;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31, j = lane % J;
-  const int64_t wid = (int64_t)blockIdx.x * (CTA / 32) + (threadIdx.x >> 5);
-  if (wid >= warps) return;
-  const int h = (int)(wid % c.heads);
-  const int64_t rest = wid / c.heads;
-  const bool val = rest & 1;
-  const int64_t row = (rest >> 1) * TPW + lane / J;
-  const Kv4Slot p = find(c, row, h);
-  const int t = (int)(p.pos & 31);
-  uint32_t w[4] = {0, 0, 0, 0};
-  float s = 0.0f;
-  if (p.at >= 0) {
-    const uint8_t* tile = c.data + p.at;
-    uint16_t hb;
-    if (!val) {
+  const int64_t row0 = (int64_t)blockIdx.x * 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES, i = lane / LANES;
+  const int h0 = blockIdx.y * span, heads = min(span, c.heads - h0);
+  const bool val = warp >= 2, rot = inverse && (val ? c.v_rot : c.k_rot);
+  const uint32_t* signs = val ? c.v_sign : c.k_sign;
+  find(c, row0, places);
+  __syncthreads();
+  const int64_t tile = places.at[i], step = (int64_t)c.tpp * c.tile_bytes;
+  const int t = places.t[i] < 0 ? 0 : places.t[i];
+  Codes<D> next;
+  uint16_t scale[NG];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = *reinterpret_cast<const uint32_t*>(tile + t * (D / 2) + k * (D / 8) + j * 4);
-      hb = *reinterpret_cast<const uint16_t*>(tile + 32 * D + (t * NG + j / (J / NG)) * 2);
-    } else {
-      const uint8_t* v = tile + 16 * D + (t >> 3) * (4 * D) + ((t & 7) >> 1) * (D / 8) + (t & 1) * (D / 16) + j * 2;
+  for (int j = 0; j < D / 32; ++j) next.w[j] = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = *reinterpret_cast<const uint16_t*>(v + 2 * k * (D / 2)) |
-               (uint32_t)*reinterpret_cast<const uint16_t*>(v + (2 * k + 1) * (D / 2)) << 16;
-      hb = *reinterpret_cast<const uint16_t*>(tile + 32 * D + 64 * NG + ((t >> 1) * NG + j / (J / NG)) * 4 +
-                                              (t & 1) * 2);
+  for (int g = 0; g < NG; ++g) scale[g] = 0;
+  auto fetch = [&](int h) {
+    if (tile < 0 || h >= heads) return;
+    const uint8_t* from = c.data + tile + (h0 + h) * step;
+    next.load(from, t, l, val);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) scale[g] = *reinterpret_cast<const uint16_t*>(from + scale_at<D, NG>(t, g, val));
+  };
+  fetch(warp & 1);
+  int64_t at = (row0 + i) * (val ? out.v_token : out.k_token) + (h0 + (warp & 1)) * (val ? out.v_head : out.k_head);
+#pragma unroll 1
+  for (int h = warp & 1; h < heads; h += 2) {
+    Codes<D> codes = next;
+    codes.join(val);
+    float s[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) s[g] = __half2float(__ushort_as_half(scale[g])) * (rot ? norm : 1.0f);
+    fetch(h + 2);
+    float z[D / 4];
+#pragma unroll
+    for (int x = 0; x < D / 4; x += 2) {
+      // 2^23 + 8 + q, less 2^23 + 8: exact
+      uint32_t u[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)  // (w & 15) ^ (2^23 + 8) in one operation
+        asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(u[k]) : "r"(codes.w[x / 8] >> (4 * ((x + k) % 8))), "r"(15u), "r"(0x4B000008u));
+      unsigned long long v, off, by;
+      asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(u[0]), "r"(u[1]));
+      asm("mov.b64 %0, {%1, %1};" : "=l"(off) : "f"(-8388616.0f));
+      asm("mov.b64 %0, {%1, %1};" : "=l"(by) : "f"(s[x / (D / 4 / NG)]));
+      asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(off));
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(by));
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(z[x]), "=f"(z[x + 1]) : "l"(v));
     }
-    s = __half2float(__ushort_as_half(hb));
+    Raw<D, F32> raw;
+    if (rot) kv4_fwht<D / 4, LANES>(z, lane);  // T^T = D H / sqrt(D)
+    raw.from_float(z);
+    if (rot && signs) raw.flip(signs, l);
+    if (places.t[i] >= 0) raw.store(const_cast<void*>(val ? out.v : out.k), at, l);
+    at += 2 * (val ? out.v_head : out.k_head);
   }
-  float z[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) z[i] = (float)((int)(w[i / 8] << (28 - 4 * (i % 8))) >> 28) * s;
-  if (inverse && (val ? c.v_rot : c.k_rot)) {
-    // T^T = D H / sqrt(D)
-    kv4_fwht<32, J>(z, lane);
-    const uint32_t* sign = val ? c.v_sign : c.k_sign;
-    if (sign) apply_signs(z, sign, j);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) z[i] *= norm;
-  }
-  if (p.seq >= 0)
-    store32<F32>(const_cast<void*>(val ? out.v : out.k),
-                 row * (val ? out.v_token : out.k_token) + h * (val ? out.v_head : out.k_head) + 32 * j, z);
 }
 
 template <class K, class... A>
-rot_status launch(K kernel, int64_t warps, cudaStream_t s, const A&... args) {
-  const int64_t ctas = (warps + CTA / 32 - 1) / (CTA / 32);
-  if (ctas > 0x7fffffff) return set_error(ROT_EUNSUPPORTED, "kv4: too many rows for one launch");
+rot_status launch(K kernel, const Kv4View& c, cudaStream_t s, const Kv4Rows& rows, float norm, const A&... args) {
+  // Heads of a CTA: two (one round of its warps) while that leaves the GPU room, up to eight once there are
+  // plenty of tokens, which then find their places once for all of them.
+  const int64_t groups = (c.T + 7) / 8;
+  int span = 2;
+  while (span < 8 && span < c.heads && groups * ((c.heads + span - 1) / span) > 8 * (int64_t)sm_count()) span *= 2;
+  const int64_t parts = (c.heads + span - 1) / span;
+  if (groups > 0x7fffffff || parts > 65535) return set_error(ROT_EUNSUPPORTED, "kv4: too many rows or heads for one launch");
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.gridDim = dim3((unsigned)groups, (unsigned)parts);
   cfg.blockDim = dim3(CTA);
   cfg.stream = s;
   cudaLaunchAttribute at{};
@@ -327,26 +488,22 @@ rot_status launch(K kernel, int64_t warps, cudaStream_t s, const A&... args) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = pdl_default() ? 1 : 0;
-  ROT_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, args...));
+  ROT_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, c, rows, norm, span, args...));
   return ROT_OK;
 }
 
 template <int D, int NG>
 rot_status run_append(const Kv4View& c, const Kv4Rows& in, cudaStream_t s) {
-  constexpr int TPW = 1024 / D;
-  const int64_t warps = (c.T + TPW - 1) / TPW * 2 * c.heads;
   const float norm = (float)(1.0 / sqrt((double)D));
-  return in.dtype == ROT_F32 ? launch(append_kernel<D, NG, true>, warps, s, c, in, norm, warps)
-                             : launch(append_kernel<D, NG, false>, warps, s, c, in, norm, warps);
+  return in.dtype == ROT_F32 ? launch(append_kernel<D, NG, true>, c, s, in, norm)
+                             : launch(append_kernel<D, NG, false>, c, s, in, norm);
 }
 
 template <int D, int NG>
 rot_status run_read(const Kv4View& c, const Kv4Rows& out, int inverse, cudaStream_t s) {
-  constexpr int TPW = 1024 / D;
-  const int64_t warps = (c.T + TPW - 1) / TPW * 2 * c.heads;
   const float norm = (float)(1.0 / sqrt((double)D));
-  return out.dtype == ROT_F32 ? launch(read_kernel<D, NG, true>, warps, s, c, out, norm, inverse, warps)
-                              : launch(read_kernel<D, NG, false>, warps, s, c, out, norm, inverse, warps);
+  return out.dtype == ROT_F32 ? launch(read_kernel<D, NG, true>, c, s, out, norm, inverse)
+                              : launch(read_kernel<D, NG, false>, c, s, out, norm, inverse);
 }
 
 }  // namespace
