@@ -161,7 +161,8 @@ struct Kv4Query {
   float* partial;           // [T * Hq, splits, D] then [T * Hq, splits, 2], NULL when splits == 1
 };
 struct Kv4Split {
-  int rows;      // query rows of a CTA (8 per n-tile)
+  int rows;      // query rows of a CTA
+  bool many;     // the kernel for many rows (kv4_rows.cu)
   int chunks;    // row chunks of a sequence and key head
   int splits;    // parts of the length
 };

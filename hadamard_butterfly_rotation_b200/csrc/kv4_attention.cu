@@ -22,35 +22,19 @@
 // P and P * scale (binary16, 2^-11 / 2 each); sums, maxima and logits are fp32. bf16 for P would round at
 // 2^-8 / 2, as coarse as the bf16 output itself.
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
-#include "kv4.cuh"
+#include "kv4_attention.cuh"
 
 namespace rotb {
 namespace {
+
+using namespace kv4;
 
 __device__ int g_kv4_attn_error = 0;
 
 constexpr int W = 4;              // warps of a CTA
 constexpr int CTA = 32 * W;
-constexpr int P_SHIFT = 7;        // P is held as p 2^7, p <= 2^8 of the reference: below 2^15
-constexpr float NINF = -__builtin_huge_valf();
-
-struct Params {
-  Kv4View c;
-  const void* q;
-  int64_t q_token, q_head;
-  __nv_bfloat16* out;
-  float* part;     // [T * Hq][splits][D]
-  float* part_ml;  // [T * Hq][splits][2]
-  int Hq, share, causal, window, chunks, splits;
-  float scale_log2;  // softmax scale * log2 e
-  float norm;        // 1 / sqrt(D)
-};
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
@@ -62,12 +46,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
   return d;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // offset nibbles u = q + 8 of two packed halves as binary16 subnormals: bits 0..3 (u 2^-24) and bits 4..7
@@ -96,41 +74,6 @@ struct Nibbles {
     return d;
   }
 };
-
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
-  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t max_half2_nan(uint32_t a, uint32_t b) {
-  const __half2 h = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// all ones in the halves that hold an infinity or a NaN
-__device__ __forceinline__ uint32_t odd_halves(uint32_t x) {
-  return ((x & 0x7c00u) == 0x7c00u ? 0xffffu : 0u) | ((x & 0x7c000000u) == 0x7c000000u ? 0xffff0000u : 0u);
-}
-
-// n 32-bit words from shared memory with the widest loads
-template <int N>
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
-  if constexpr (N % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                   : "r"(addr + 4 * i));
-  } else if constexpr (N == 2) {
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-  } else {
-    static_assert(N == 1);
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
-  }
-}
 
 // Waits for a stage's copy, for at most about a second; false where it gave up
 __device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity) {
@@ -192,33 +135,9 @@ struct Lay {
   static constexpr int SMEM = O_BAR + W * ST * 8;
 };
 
-// Final row: joined sums o (lane's D/32 coordinates) over l, back through U^T, to bf16
-template <int D>
-__device__ __forceinline__ void finish_row(const Params& p, float (&o)[D / 32], float l, int64_t row, int lane) {
-  constexpr int V = D / 32;
-  const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros (a NaN sum stays)
-  float scale = inv;
-  if (p.c.v_rot) {
-    kv4_fwht<V, 32>(o, lane);
-    scale *= p.norm;
-    if (p.c.v_sign) {
-#pragma unroll
-      for (int i = 0; i < V; i += 2) {
-        const uint32_t w = __ldg(p.c.v_sign + (lane * V + i) / 2);
-        o[i] = kv4_signed(o[i], w, 0);
-        o[i + 1] = kv4_signed(o[i + 1], w, 1);
-      }
-    }
-  }
-  uint32_t w[V / 2];
-#pragma unroll
-  for (int i = 0; i < V; i += 2) w[i / 2] = kv4_pack_bf16(o[i] * scale, o[i + 1] * scale);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D + lane * V);
-  if constexpr (V == 2) dst[0] = w[0];
-  else if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
+#ifndef KV4_MANY
+#define KV4_MANY 64
+#endif
 #ifndef KV4_HALF
 #define KV4_HALF 128
 #endif
@@ -834,32 +753,11 @@ __global__ void __launch_bounds__(JOIN_CTA) join_kernel(const __grid_constant__ 
   finish_row<D>(p, o, l, row, lane);
 }
 
-// KERNEL's shared memory is allowed once per device.
-template <auto KERNEL>
-rot_status launch(int64_t ctas, int threads, int smem, cudaStream_t s, const Params& p) {
-  if (ctas > 0x7fffffff) return set_error(ROT_EUNSUPPORTED, "kv4_attention: too many rows for one launch");
-  if (smem > 48 * 1024) {
-    static std::atomic<uint64_t> allowed{0};
-    int dev = 0;
-    ROT_CUDA_TRY(cudaGetDevice(&dev));
-    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (!bit || !(allowed.load(std::memory_order_relaxed) & bit)) {
-      ROT_CUDA_TRY(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-      allowed.fetch_or(bit);
-    }
-  }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = pdl_default() ? 1 : 0;
-  ROT_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, p));
-  return ROT_OK;
+template <int D>
+rot_status join(const Params& p, cudaStream_t s) {
+  // one warp walks up to 16 parts in two rounds of loads; more parts are spread over eight
+  return p.splits > 16 ? launch<join_kernel<D, 8>>(p.c.T * p.Hq, JOIN_CTA, 0, s, p)
+                       : launch<join_kernel<D, 1>>((p.c.T * p.Hq + 7) / 8, JOIN_CTA, 0, s, p);
 }
 
 template <int D, int NG, int NT>
@@ -868,10 +766,7 @@ rot_status run(const Params& p, bool q_f32, cudaStream_t s) {
   constexpr int smem = Lay<D, NG, NT>::SMEM;
   rot_status st = q_f32 ? launch<attention_kernel<D, NG, NT, true>>(ctas, CTA, smem, s, p)
                         : launch<attention_kernel<D, NG, NT, false>>(ctas, CTA, smem, s, p);
-  if (st || p.splits == 1) return st;
-  // one warp walks up to 16 parts in two rounds of loads; more parts are spread over eight
-  return p.splits > 16 ? launch<join_kernel<D, 8>>(p.c.T * p.Hq, JOIN_CTA, 0, s, p)
-                       : launch<join_kernel<D, 1>>((p.c.T * p.Hq + 7) / 8, JOIN_CTA, 0, s, p);
+  return st || p.splits == 1 ? st : join<D>(p, s);
 }
 
 template <int D, int NG>
@@ -888,8 +783,25 @@ Kv4Split kv4_split(int D, int B, int heads, int share, int window, int64_t max_n
   Kv4Split sp{};
   if (window > 0) max_len = std::min(max_len, max_new + window);
   const int64_t rows = max_new * share;
-  sp.rows = rows > 8 && D < 256 ? 16 : 8;
+  sp.many = D < 256 && rows > KV4_MANY;
+  sp.rows = sp.many ? KV4_ROWS : rows > 8 && D < 256 ? 16 : 8;
   sp.chunks = (int)std::min<int64_t>(std::max<int64_t>((rows + sp.rows - 1) / sp.rows, 1), 1 << 20);
+  if (sp.many) {
+    // one CTA to an SM: the number of parts that wastes least of the last round, a CTA's start and end counted
+    // as three steps of 128 tokens
+    const int64_t units = std::max<int64_t>((int64_t)B * heads * sp.chunks, 1), steps = std::max<int64_t>((max_len + 127) / 128, 1);
+    double best = 0.0;
+    sp.splits = 1;
+    for (int64_t n = 1; n <= 16 && n <= std::max<int64_t>(steps / 4, 1); ++n) {
+      const int64_t rounds = (units * n + sms - 1) / sms;
+      const double use = (double)(units * steps) / (double)(rounds * sms * ((steps + n - 1) / n + 3));
+      if (use > best * 1.02) {
+        best = use;
+        sp.splits = (int)n;
+      }
+    }
+    return sp;
+  }
   // Parts of the length: as many CTAs as fit at once, with at least four tiles to a warp; up to three times
   // as many, which evens out uneven lengths, where a warp keeps sixteen tiles. (A CTA's own start and end
   // cost as much as about three of a warp's tiles.)
@@ -920,6 +832,10 @@ rot_status kv4_attention_launch(const Kv4View& c, int D, int NG, const Kv4Query&
   p.scale_log2 = q.scale * 1.4426950408889634f;
   p.norm = (float)(1.0 / sqrt((double)D));
   const bool f32 = q.q_dtype == ROT_F32;
+  if (sp.many) {
+    const rot_status st = kv4_rows_launch(p, D, NG, f32, s);
+    return st || p.splits == 1 ? st : D == 64 ? join<64>(p, s) : join<128>(p, s);
+  }
   switch (D * 16 + NG) {
     case 64 * 16 + 2: return run_rows<64, 2>(p, f32, sp.rows, s);
     case 64 * 16 + 1: return run_rows<64, 1>(p, f32, sp.rows, s);
@@ -935,6 +851,8 @@ rot_status kv4_attention_launch(const Kv4View& c, int D, int NG, const Kv4Query&
 }
 
 rot_status kv4_attention_fetch_device_error() {
+  const rot_status rows = kv4_rows_fetch_device_error();
+  if (rows) return rows;
   int v = 0;
   ROT_CUDA_TRY(cudaMemcpyFromSymbol(&v, g_kv4_attn_error, sizeof(int)));
   if (v) {

@@ -1,0 +1,136 @@
+// What the attention kernels over the 4-bit cache share: their arguments, a row's end, small device pieces
+// and the launch.
+#pragma once
+
+#include <atomic>
+
+#include "kv4.cuh"
+
+namespace rotb {
+namespace kv4 {
+
+constexpr int P_SHIFT = 7;        // P is held as p 2^7, p <= 2^8 of the reference: below 2^15
+constexpr float NINF = -__builtin_huge_valf();
+
+struct Params {
+  Kv4View c;
+  const void* q;
+  int64_t q_token, q_head;
+  __nv_bfloat16* out;
+  float* part;     // [T * Hq][splits][D]
+  float* part_ml;  // [T * Hq][splits][2]
+  int Hq, share, causal, window, chunks, splits;
+  float scale_log2;  // softmax scale * log2 e
+  float norm;        // 1 / sqrt(D)
+};
+
+#ifdef __CUDACC__
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t max_half2_nan(uint32_t a, uint32_t b) {
+  const __half2 h = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// all ones in the halves that hold an infinity or a NaN
+__device__ __forceinline__ uint32_t odd_halves(uint32_t x) {
+  return ((x & 0x7c00u) == 0x7c00u ? 0xffffu : 0u) | ((x & 0x7c000000u) == 0x7c000000u ? 0xffff0000u : 0u);
+}
+
+// n 32-bit words from shared memory with the widest loads
+template <int N>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "r"(addr + 4 * i));
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  } else {
+    static_assert(N == 1);
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+  }
+}
+
+// Final row: joined sums o (lane's D/32 coordinates) over l, back through U^T, to bf16
+template <int D>
+__device__ __forceinline__ void finish_row(const Params& p, float (&o)[D / 32], float l, int64_t row, int lane) {
+  constexpr int V = D / 32;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // nothing seen: zeros (a NaN sum stays)
+  float scale = inv;
+  if (p.c.v_rot) {
+    kv4_fwht<V, 32>(o, lane);
+    scale *= p.norm;
+    if (p.c.v_sign) {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const uint32_t w = __ldg(p.c.v_sign + (lane * V + i) / 2);
+        o[i] = kv4_signed(o[i], w, 0);
+        o[i + 1] = kv4_signed(o[i + 1], w, 1);
+      }
+    }
+  }
+  uint32_t w[V / 2];
+#pragma unroll
+  for (int i = 0; i < V; i += 2) w[i / 2] = kv4_pack_bf16(o[i] * scale, o[i + 1] * scale);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D + lane * V);
+  if constexpr (V == 2) dst[0] = w[0];
+  else if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+
+// KERNEL's shared memory is allowed once per device.
+template <auto KERNEL>
+rot_status launch(int64_t ctas, int threads, int smem, cudaStream_t s, const Params& p) {
+  if (ctas > 0x7fffffff) return set_error(ROT_EUNSUPPORTED, "kv4_attention: too many rows for one launch");
+  if (smem > 48 * 1024) {
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    ROT_CUDA_TRY(cudaGetDevice(&dev));
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!bit || !(allowed.load(std::memory_order_relaxed) & bit)) {
+      ROT_CUDA_TRY(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+      allowed.fetch_or(bit);
+    }
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = pdl_default() ? 1 : 0;
+  ROT_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, p));
+  return ROT_OK;
+}
+
+#endif
+
+}  // namespace kv4
+
+// Many query rows to a key head (kv4_rows.cu)
+rot_status kv4_rows_launch(const kv4::Params& p, int D, int NG, bool q_f32, cudaStream_t s);
+constexpr int KV4_ROWS = 256;  // query rows of its CTA
+rot_status kv4_rows_fetch_device_error();
+
+}  // namespace rotb

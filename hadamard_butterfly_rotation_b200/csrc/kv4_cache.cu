@@ -15,8 +15,8 @@ namespace {
 __device__ int g_kv4_cache_error = 0;
 
 constexpr int CTA = 128;  // two warps for keys, two for values
-// CTAs that an SM holds, by the registers that are left to a thread: appending 12.9 k tokens of 8 x 128 took
-// 22 us with 4 (128 registers), 25 us with 5 and 29 us with 6, reading 72 k of them 96, 89 and 86 us.
+// CTAs that an SM holds, by the registers that are left to a thread: appending 9.2 k tokens of 8 x 128 took
+// 22 us with 4 (128 registers), 25 us with 5 and 29 us with 6, reading 65 k of them 96, 89 and 86 us.
 constexpr int append_ctas(int D) { return D == 256 ? 2 : 4; }
 constexpr int read_ctas(int D) { return D == 256 ? 2 : 6; }
 
