@@ -10,9 +10,10 @@
 //   O += P V     A is P in TMEM, B is V in shared memory as it lies in the cache, tokens by rows of
 //                coordinates (N-major); O stays in TMEM and is rescaled only when a row's reference rises by
 //                more than 2^8
-// Warps 0..7 are the softmax of the two row tiles, 8..11 fetch and unpack (each one cache tile of 32 tokens per
-// step, with a bulk copy of its own in flight), warp 12 issues the MMAs. While one row tile is in its softmax, the
-// tensor pipe works on the other. The unpacking is paid once for 256 rows.
+// Warps 0..7 are the softmax of the two row tiles, 8..11 fetch and unpack keys, 12..15 values (each one cache
+// tile of 32 tokens per step, with a bulk copy of its own in flight), warp 16 issues the MMAs. While one row tile is
+// in its softmax, the tensor pipe works on the other. The unpacking is paid once for 256 rows; with keys and values
+// in the same warps a step waited for the values' stage before the next keys could be unpacked.
 // Codes become binary16 values code * scale 2^-e, e the exponent of the largest scale of the 32 tokens, so that
 // any binary16 scale stays in range: key exponents multiply the logits, value exponents the probabilities.
 // Roundings below 32 bits: query, key and value operands and P, 2^-11 / 2 relative each. The order of coordinates
@@ -30,7 +31,7 @@ using namespace kv4;
 __device__ int g_kv4_rows_error = 0;
 
 constexpr int ROWS = KV4_ROWS, TOK = 128;
-constexpr int SOFT = 8, UNP = 4, WARPS = SOFT + UNP + 1, CTA = 32 * WARPS;
+constexpr int SOFT = 8, UNP = 4, WARPS = SOFT + 2 * UNP + 1, CTA = 32 * WARPS;
 constexpr unsigned long long WAIT_NS = 1000000000ull;
 
 template <int D, int NG>
@@ -40,19 +41,20 @@ struct Lay {
   static constexpr int O_K = O_Q + ROWS * D * 2;       // [2 stages][D / 64][128 tokens][128 bytes]
   static constexpr int O_V = O_K + 2 * KV;             // the same; both hold O at the end, fp32 [256][D]
   static constexpr int CODES = 16 * D;                 // packed keys, or values, of a cache tile
-  static constexpr int SCALES = 128 * NG;              // its scales
-  static constexpr int RAW = 2 * CODES + 2 * SCALES;   // keys, values, two sets of scales
-  static constexpr int O_RAW = O_V + 2 * KV;           // [UNP]
-  static constexpr int O_FAC = O_RAW + UNP * RAW;      // per row: logit factor
+  static constexpr int SCALES = 64 * NG;               // their scales
+  static constexpr int RAW = CODES + 2 * SCALES;       // an unpacking warp's: codes, two sets of scales
+  static constexpr int O_RAW = O_V + 2 * KV;           // [2 UNP]
+  static constexpr int O_FAC = O_RAW + 2 * UNP * RAW;  // per row: logit factor
   static constexpr int O_SEEN = O_FAC + ROWS * 4;      // per row: the tokens that it sees
   static constexpr int O_ML = O_SEEN + ROWS * 8;       // per row: reference and sum at the end
   static constexpr int O_EXP = O_ML + ROWS * 8;        // [4 steps][UNP]: 2^key exponent, value exponent
   static constexpr int O_ODD = O_EXP + 4 * UNP * 8;    // [4 steps][UNP][NG]: tokens with NaN or infinite value scales
-  static constexpr int O_BAR = O_ODD + 4 * UNP * NG * 4;
+  static constexpr int O_FLAG = O_ODD + 4 * UNP * NG * 4;  // [4 steps][UNP]: whether any of these is set
+  static constexpr int O_BAR = O_FLAG + 4 * UNP * 4;
   static constexpr int BARS = 2 + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 2 * UNP;
   static constexpr int O_TMEM = O_BAR + BARS * 8;
   static constexpr int SMEM = O_TMEM + 16 + 1024;      // (the base is rounded up to 1024)
-  static_assert(O_ODD % 8 == 0 && O_BAR % 8 == 0 && SMEM <= 227 * 1024, "shared memory");
+  static_assert(O_ODD % 8 == 0 && O_FLAG % 16 == 0 && O_BAR % 8 == 0 && SMEM <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
@@ -179,14 +181,14 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&w)[4]) {
 }
 
 // The eight codes of a word as binary16 code * scale, pairs (0, 4) (1, 5) (2, 6) (3, 7): exact integers out of the
-// mantissa of 1024 + u and 1024 + 16 u, then one rounding in the product
+// mantissa of 1024 + u and 1024 + 16 u, then one rounding in the product. ((w & mask) ^ flip is one operation.)
 __device__ __forceinline__ void unpack(uint32_t w, uint32_t scale2, uint32_t (&v)[4]) {
   const uint32_t x = w >> 8;
   uint32_t t[4];
-  t[0] = (w & 0x000F000Fu) ^ 0x64086408u;
-  t[1] = (w & 0x00F000F0u) ^ 0x64806480u;
-  t[2] = (x & 0x000F000Fu) ^ 0x64086408u;
-  t[3] = (x & 0x00F000F0u) ^ 0x64806480u;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(t[0]) : "r"(w), "r"(0x000F000Fu), "r"(0x64086408u));
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(t[1]) : "r"(w), "r"(0x00F000F0u), "r"(0x64806480u));
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(t[2]) : "r"(x), "r"(0x000F000Fu), "r"(0x64086408u));
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(t[3]) : "r"(x), "r"(0x00F000F0u), "r"(0x64806480u));
   const __half2 off = __half2half2(__ushort_as_half(0xE408)), off16 = __half2half2(__ushort_as_half(0xD480));  // -1032, -72
   const __half2 by16 = __half2half2(__ushort_as_half(0x2C00)), s = *reinterpret_cast<const __half2*>(&scale2);  // 1 / 16
 #pragma unroll
@@ -195,6 +197,15 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t scale2, uint32_t (&v
     const __half2 c = __hmul2(i & 1 ? __hfma2(u, by16, off16) : __hadd2(u, off), s);
     v[i] = *reinterpret_cast<const uint32_t*>(&c);
   }
+}
+
+__device__ __forceinline__ float max3f(float a, float b, float c) { return fmaxf(a, fmaxf(b, c)); }
+
+// a block's exponents and, whether any value scale of its step stands for NaN
+__device__ __forceinline__ float2 lds2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
 }
 
 template <int D, int NG, bool QF32>
@@ -212,8 +223,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
   uint64_t* sfull = xfull + 4;                                     // [2] S of a row tile -> softmax
   uint64_t* pfull = sfull + 2;                                     // [2] P of a row tile -> MMA
   uint64_t* odone = pfull + 2;                                     // [2] P V of a row tile done -> softmax
-  uint64_t* rawk = odone + 2;                                      // [UNP] packed keys and scales
-  uint64_t* rawv = rawk + UNP;                                     // [UNP] packed values
+  uint64_t* raws = odone + 2;                                      // [2 UNP] packed keys, then packed values
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::O_TMEM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::O_TMEM + 8);
   float* r_fac = reinterpret_cast<float*>(smem + L::O_FAC);
@@ -221,6 +231,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
   float2* r_ml = reinterpret_cast<float2*>(smem + L::O_ML);
   float2* exps = reinterpret_cast<float2*>(smem + L::O_EXP);
   uint32_t* odds = reinterpret_cast<uint32_t*>(smem + L::O_ODD);
+  uint32_t* flag = reinterpret_cast<uint32_t*>(smem + L::O_FLAG);
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -232,11 +243,8 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
       mbar_init(&pfull[s], 4);
       mbar_init(&odone[s], 1);
     }
-    for (int s = 0; s < 4; ++s) mbar_init(&xfull[s], UNP);
-    for (int s = 0; s < UNP; ++s) {
-      mbar_init(&rawk[s], 1);
-      mbar_init(&rawv[s], 1);
-    }
+    for (int s = 0; s < 4; ++s) mbar_init(&xfull[s], 2 * UNP);
+    for (int s = 0; s < 2 * UNP; ++s) mbar_init(&raws[s], 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
   int64_t first, first_pos;
   const int n_new = kv4_new_rows(p.c, b, &first, &first_pos);
   const int n_rows = n_new * p.share, len = max(p.c.lens[b], 0), pos0 = (int)first_pos;
-  uint32_t got = 0;   // tiles that an unpacking warp has fetched: the phase of rawk and rawv
+  uint32_t got = 0;   // tiles that an unpacking warp has fetched: the phase of its raws
   uint32_t step = 0;  // steps of 128 tokens since the start: what the barriers' phases go by
   bool ok = true;
 
@@ -280,62 +288,79 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
     const int n = to - from, tok_a = (step_a + from) * TOK;
 
     // ---- query rows: rotate, scale to binary16 by a power of two, K-major
-    for (int rr = warp; rr < tiles_q * 128; rr += WARPS) {
-      const int row = row0 + rr;
-      float v[V];
+    constexpr int BATCH = 4;  // rows in flight to a warp
+    for (int r0 = warp * BATCH; r0 < tiles_q * 128; r0 += WARPS * BATCH) {
+      float v[BATCH][V], m[BATCH];
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = 0.0f;
-      if (row < n_rows) {
-        const int64_t at = (first + row / p.share) * p.q_token + ((int64_t)h * p.share + row % p.share) * p.q_head + lane * V;
+      for (int u = 0; u < BATCH; ++u) {
+        const int row = row0 + r0 + u;
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          if constexpr (QF32) {
-            const float2 x = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p.q) + at + i));
-            v[i] = x.x;
-            v[i + 1] = x.y;
-          } else {
-            const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + at + i));
-            v[i] = __uint_as_float(x << 16);
-            v[i + 1] = __uint_as_float(x & 0xffff0000u);
+        for (int i = 0; i < V; ++i) v[u][i] = 0.0f;
+        if (row < n_rows) {
+          const int64_t at = (first + row / p.share) * p.q_token + ((int64_t)h * p.share + row % p.share) * p.q_head + lane * V;
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            if constexpr (QF32) {
+              const float2 x = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p.q) + at + i));
+              v[u][i] = x.x;
+              v[u][i + 1] = x.y;
+            } else {
+              const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + at + i));
+              v[u][i] = __uint_as_float(x << 16);
+              v[u][i + 1] = __uint_as_float(x & 0xffff0000u);
+            }
           }
         }
       }
-      float fac = p.scale_log2;
       if (p.c.k_rot) {
         if (p.c.k_sign) {
 #pragma unroll
           for (int i = 0; i < V; i += 2) {
             const uint32_t w = __ldg(p.c.k_sign + (lane * V + i) / 2);
-            v[i] = kv4_signed(v[i], w, 0);
-            v[i + 1] = kv4_signed(v[i + 1], w, 1);
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+              v[u][i] = kv4_signed(v[u][i], w, 0);
+              v[u][i + 1] = kv4_signed(v[u][i + 1], w, 1);
+            }
           }
         }
-        kv4_fwht<V, 32>(v, lane);
-        fac *= p.norm;
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) kv4_fwht<V, 32>(v[u], lane);
       }
-      float m = 0.0f;
+      const float fac = p.c.k_rot ? p.scale_log2 * p.norm : p.scale_log2;
 #pragma unroll
-      for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(v[i]));
+      for (int u = 0; u < BATCH; ++u) {
+        m[u] = 0.0f;
 #pragma unroll
-      for (int x = 1; x < 32; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-      const int e = m > 0.0f ? min(max(141 - (int)(__float_as_uint(m) >> 23), -100), 100) : 0;
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int d = lane * V + i, q8 = d >> 3, place = 2 * (d & 3) + ((d >> 2) & 1);
-        uint8_t* at = smem + L::O_Q + (rr >> 7) * (128 * D * 2) + (q8 >> 3) * (128 * 128) + (rr & 127) * 128 +
-                      (((q8 & 7) ^ (rr & 7)) << 4) + place * 2;
-        *reinterpret_cast<__half*>(at) = __float2half_rn(v[i] * up);
+        for (int i = 0; i < V; ++i) m[u] = fmaxf(m[u], fabsf(v[u][i]));
       }
-      if (lane == 0) {
-        r_fac[rr] = fac * __uint_as_float((uint32_t)(127 - e) << 23);
-        int2 seen = make_int2(0, high);  // the tokens that the row sees: [x, y)
-        if (row < n_rows) {
-          const int pos = pos0 + row / p.share;
-          if (p.causal) seen.y = min(high, pos + 1);
-          if (p.window) seen.x = max(0, pos - p.window + 1);
+#pragma unroll
+      for (int x = 1; x < 32; x *= 2)
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], x));
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        const int rr = r0 + u, row = row0 + rr;
+        const int e = m[u] > 0.0f ? min(max(141 - (int)(__float_as_uint(m[u]) >> 23), -100), 100) : 0;
+        // (a negative softmax scale turns the query around, so that the factor is not negative)
+        const float up = copysignf(__uint_as_float((uint32_t)(127 + e) << 23), fac);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int d = lane * V + i, q8 = d >> 3, place = 2 * (d & 3) + ((d >> 2) & 1);
+          uint8_t* at = smem + L::O_Q + (rr >> 7) * (128 * D * 2) + (q8 >> 3) * (128 * 128) + (rr & 127) * 128 +
+                        (((q8 & 7) ^ (rr & 7)) << 4) + place * 2;
+          *reinterpret_cast<__half*>(at) = __float2half_rn(v[u][i] * up);
         }
-        r_seen[rr] = seen;
+        if (lane == 0) {
+          r_fac[rr] = fabsf(fac) * __uint_as_float((uint32_t)(127 - e) << 23);
+          int2 seen = make_int2(0, high);  // the tokens that the row sees: [x, y)
+          if (row < n_rows) {
+            const int pos = pos0 + row / p.share;
+            if (p.causal) seen.y = min(high, pos + 1);
+            if (p.window) seen.x = max(0, pos - p.window + 1);
+          }
+          r_seen[rr] = seen;
+        }
       }
     }
     fence_async();
@@ -358,37 +383,42 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
           if (!ok) break;
           tc_after();
           const bool edge = __any_sync(0xffffffffu, tok < seen.x || tok + TOK > seen.y);
-          const float2* ex = exps + (g & 3) * UNP;
-          float top = NINF, vtop = vref;
-          uint32_t s[32];
-          auto masked = [&](int c) {
-            if (edge) {
-              const int lo = seen.x - tok - 32 * c, hi = seen.y - tok - 32 * c;
+          float f[4], shift[4], top = NINF, vtop = vref;  // of the step's four cache tiles
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (k < lo || k >= hi) s[k] = __float_as_uint(NINF);
-            }
+          for (int c = 0; c < 4; ++c) {
+            const float2 ex = lds2(smem_u32(exps) + ((g & 3) * UNP + c) * 8);
+            f[c] = fac * ex.x;
+            shift[c] = ex.y;
+            vtop = fmaxf(vtop, ex.y);
+          }
+          // ---- a row's largest logit
+          uint32_t s[32];
+          auto masked = [&](uint32_t (&x)[32], int c) {
+            const int lo = seen.x - tok - 32 * c, hi = seen.y - tok - 32 * c;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (k < lo || k >= hi) x[k] = __float_as_uint(NINF);
           };
-          // a row's largest logit (fac < 0 turns a masked one around: masked after the product)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             tmem_ld32(s_at + 32 * c, s);
             wait_ld();
-            const float f = fac * ex[c].x;
-            vtop = fmaxf(vtop, ex[c].y);
+            if (edge) masked(s, c);
+            float m = __uint_as_float(s[0]), m2 = __uint_as_float(s[1]);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * f);
-            masked(c);
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
+            for (int k = 2; k < 32; k += 4) {
+              m = max3f(m, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+              if (k + 2 < 32) m2 = max3f(m2, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+            }
+            if (shift[c] != NINF) top = fmaxf(top, fmaxf(m, m2) * f[c]);  // (f >= 0)
           }
           if (__any_sync(0xffffffffu, top > ref + 8.0f || vtop > vref)) {
             const float now = fmaxf(ref, top);
-            const float f = ref == NINF ? 0.0f : ex2(ref - now);
-            const float fo = f * ex2(vref - vtop);
+            const float down = ref == NINF ? 0.0f : ex2(ref - now);
+            const float down_o = down * ex2(vref - vtop);
             ref = now;
             vref = vtop;
-            sum *= f;
+            sum *= down;
             if (i > 0) {
               ok = wait(&odone[q], (g - 1) & 1, abort_flag);
               if (!ok) break;
@@ -398,45 +428,56 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
                 tmem_ld32(o_at + c, s);
                 wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * fo);
+                for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * down_o);
                 tmem_st32(o_at + c, s);
               }
               wait_st();
             }
           }
+          // ---- P 2^(7 + the value exponent over the reference one)
           const float base = (float)P_SHIFT - fmaxf(ref, -3.0e38f);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             tmem_ld32(s_at + 32 * c, s);
             wait_ld();
-            const float f = fac * ex[c].x, shift = ex[c].y - vref, at = base + shift;
-            float part = 0.0f;
+            const float up = shift[c] - vref, at = base + up;
+            unsigned long long f2, at2, part = 0;
+            asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f[c]));
+            asm("mov.b64 %0, {%1, %1};" : "=l"(at2) : "f"(at));
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(fmaf(__uint_as_float(s[k]), f, at));
-            masked(c);
+            for (int k = 0; k < 32; k += 2) {
+              unsigned long long x;
+              asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(s[k]), "r"(s[k + 1]));
+              asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(x), "l"(f2), "l"(at2));
+              asm("mov.b64 {%0, %1}, %2;" : "=r"(s[k]), "=r"(s[k + 1]) : "l"(x));
+            }
+            if (edge) masked(s, c);
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
-              const float a = ex2(__uint_as_float(s[k])), d = ex2(__uint_as_float(s[k + 1]));
-              part += a + d;
-              pk[k / 2] = pack_half(a, d);
+              const float x = ex2(__uint_as_float(s[k])), y = ex2(__uint_as_float(s[k + 1]));
+              unsigned long long xy;
+              asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
+              asm("add.rn.f32x2 %0, %1, %2;" : "=l"(part) : "l"(part), "l"(xy));
+              pk[k / 2] = pack_half(x, y);
             }
-            sum = fmaf(part, ex2(-shift), sum);
+            float pa, pb;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(pa), "=f"(pb) : "l"(part));
+            sum = fmaf(pa + pb, ex2(fminf(-up, 100.0f)), sum);
             tmem_st16(s_at + 16 * c, pk);
           }
-          // value scales that stand for NaN: their groups, in the rows that see the token
-          const uint32_t* od = odds + (g & 3) * UNP * NG;
-#pragma unroll 1
-          for (int w = 0; w < UNP; ++w)
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
-              const uint32_t bits = od[w * NG + gr];
-              if (bits) {
+          // ---- value scales that stand for NaN (rare): their groups, in the rows that see the token
+          uint32_t flags[4];
+          lds<4>(smem_u32(flag) + (g & 3) * 16, flags);
+          if (flags[0] | flags[1] | flags[2] | flags[3]) {
+            const uint32_t* od = odds + (g & 3) * UNP * NG;
+            for (int w = 0; w < UNP; ++w)
+              for (int gr = 0; flag[(g & 3) * UNP + w] && gr < NG; ++gr) {
                 const int lo = min(max(seen.x - tok - 32 * w, 0), 32), hi = min(max(seen.y - tok - 32 * w, 0), 32);
                 const uint32_t in = hi > lo ? (hi == 32 ? ~0u : (1u << hi) - 1) & ~((1u << lo) - 1) : 0u;
-                if (bits & in) poison |= 1u << gr;
+                if (od[w * NG + gr] & in) poison |= 1u << gr;
               }
-            }
+          }
           wait_st();
           tc_before();
           __syncwarp();
@@ -475,160 +516,159 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         }
         tc_before();
       }
-    } else if (warp < SOFT + UNP) {
-      // ======================= fetch and unpack: cache tile w of every step
-      const int w = warp - SOFT, r = lane >> 2, c = lane & 3;
-      const uint32_t raw = smem_u32(smem) + L::O_RAW + w * L::RAW;
-      const uint32_t raw_v = raw + L::CODES, raw_s = raw + 2 * L::CODES;
-      int64_t my_at = -1;
-      auto at_of = [&](int i) -> int64_t {  // the tile of step i, or -1; lanes look 32 steps ahead
+    } else if (warp < SOFT + 2 * UNP) {
+      // ======================= fetch and unpack: cache tile w of every step, its keys or its values
+      const int w = (warp - SOFT) % UNP, r = lane >> 2, c = lane & 3;
+      const bool val = warp >= SOFT + UNP;
+      // packed codes and two sets of scales, the next step's on their way while this one's are in use
+      const uint32_t raw = smem_u32(smem) + L::O_RAW + (warp - SOFT) * L::RAW, raw_s = raw + L::CODES;
+      uint64_t* rawbar = raws + (warp - SOFT);
+      uint64_t *full = val ? vfull : kfull, *empty = val ? vempty : kempty;
+      int64_t my_at = -1;  // the lane's tile out of the next 32 steps
+      auto at_of = [&](int i) -> int64_t {
+        if (i >= n) return -1;
+        if ((i & 31) == 0) {
+          const int mine = i + lane, tok = tok_a + mine * TOK + 32 * w;
+          my_at = -1;
+          if (mine < n && tok < high) {
+            my_at = kv4_tile_at(p.c, b, tok >> 5, h);
+            if (my_at < 0) atomicExch(&g_kv4_rows_error, (int)ROT_EINVAL);
+          }
+        }
         return __shfl_sync(0xffffffffu, my_at, i & 31);
       };
-      auto look = [&](int i) {
-        if (i & 31) return;
-        const int mine = i + lane, tok = tok_a + mine * TOK + 32 * w;
-        my_at = -1;
-        if (mine < n && tok < high) {
-          my_at = kv4_tile_at(p.c, b, tok >> 5, h);
-          if (my_at < 0) atomicExch(&g_kv4_rows_error, (int)ROT_EINVAL);
-        }
-      };
-      auto load_k = [&](int i, int64_t at) {
+      auto load = [&](int i, int64_t at) {
         if (at >= 0 && lane == 0) {
-          mbar_expect(&rawk[w], L::CODES + L::SCALES);
-          bulk_load(raw, p.c.data + at, L::CODES, &rawk[w]);
-          bulk_load(raw_s + (i & 1) * L::SCALES, p.c.data + at + 2 * L::CODES, L::SCALES, &rawk[w]);
+          const uint8_t* from = p.c.data + at;
+          mbar_expect(rawbar, L::CODES + L::SCALES);
+          bulk_load(raw, from + (val ? L::CODES : 0), L::CODES, rawbar);
+          bulk_load(raw_s + (i & 1) * L::SCALES, from + 2 * L::CODES + (val ? L::SCALES : 0), L::SCALES, rawbar);
         }
       };
-      auto load_v = [&](int64_t at) {
-        if (at >= 0 && lane == 0) {
-          mbar_expect(&rawv[w], L::CODES);
-          bulk_load(raw_v, p.c.data + at + L::CODES, L::CODES, &rawv[w]);
-        }
-      };
-      look(0);
-      int64_t at = n > 0 ? at_of(0) : -1;
-      load_k(0, at);
-      load_v(at);
+      int64_t at = at_of(0);
+      load(0, at);
       for (int i = 0; i < n && ok; ++i) {
         const uint32_t g = step + i, s = g & 1;
         const int tok = tok_a + i * TOK + 32 * w;
-        int64_t next = -1;
-        if (i + 1 < n) {
-          look(i + 1);
-          next = at_of(i + 1);
-        }
+        const int64_t next = at_of(i + 1);
         const bool here = at >= 0;
         const uint32_t sc = raw_s + (i & 1) * L::SCALES;
-        // ---- exponents of the largest scales (tokens outside the sequence do not count)
-        float kx = 1.0f, vx = -14.0f, kdown = 1.0f, vdown = 1.0f;
+        // ---- the exponent of the largest scale (tokens outside the sequence do not count): scales are not negative,
+        // so their bits compare as integers, infinities and NaN on top. A tile that is not there has a value
+        // exponent of -inf, with which its probabilities vanish.
+        int ex = 0;
+        uint32_t odd = 0;
         if (here) {
-          ok = wait(&rawk[w], got & 1, abort_flag);
+          ok = wait(rawbar, got & 1, abort_flag);
           if (!ok) break;
-          // this lane's token: its NG key scales, and by pairs (lane / 2) its value scales
+          // the lane's token: a key's scales follow one another, a value's are the pair's, every second
           const bool in = tok + lane >= low && tok + lane < high;
-          uint16_t vsc[NG];
-          float kb = 0.0f, vb = 0.0f;
+          uint32_t top = 0, fine = 0;
 #pragma unroll
           for (int gr = 0; gr < NG; ++gr) {
-            uint16_t a;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a) : "r"(sc + (lane * NG + gr) * 2));
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(vsc[gr]) : "r"(sc + 64 * NG + ((lane >> 1) * NG + gr) * 4 + (lane & 1) * 2));
-            if (in && (a & 0x7c00u) != 0x7c00u) kb = fmaxf(kb, __half2float(__ushort_as_half(a)));
-            const bool odd = (vsc[gr] & 0x7c00u) == 0x7c00u;
-            if (in && !odd) vb = fmaxf(vb, __half2float(__ushort_as_half(vsc[gr])));
-            const uint32_t bits = __ballot_sync(0xffffffffu, in && odd);
-            if (lane == 0) odds[((g & 3) * UNP + w) * NG + gr] = bits;
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];"
+                         : "=h"(x)
+                         : "r"(sc + (val ? ((lane >> 1) * NG + gr) * 4 + (lane & 1) * 2 : (lane * NG + gr) * 2)));
+            const uint32_t bits = in ? x & 0x7fffu : 0u;
+            top = max(top, bits);
+            fine = max(fine, bits < 0x7c00u ? bits : 0u);
           }
-#pragma unroll
-          for (int x = 1; x < 32; x *= 2) {
-            kb = fmaxf(kb, __shfl_xor_sync(0xffffffffu, kb, x));
-            vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, x));
-          }
-          const int ke = min(max((int)(__float_as_uint(kb) >> 23) - 126, -14), 16);  // kb <= 2^ke
-          const int ve = min(max((int)(__float_as_uint(vb) >> 23) - 126, -14), 16);
-          kx = __uint_as_float((uint32_t)(127 + ke) << 23);
-          kdown = __uint_as_float((uint32_t)(127 - ke) << 23);
-          vx = (float)ve;
-          vdown = __uint_as_float((uint32_t)(127 - ve) << 23);
-        } else if (lane < NG) {
-          odds[((g & 3) * UNP + w) * NG + lane] = 0;
-        }
-        if (lane == 0) exps[(g & 3) * UNP + w] = make_float2(kx, vx);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&xfull[g & 3]);
-        // ---- keys (tokens outside the sequence give logits that the softmax masks)
-        ok = wait(&kempty[s], ((g >> 1) & 1) ^ 1, abort_flag);
-        if (!ok) break;
-        const uint32_t k_to = smem_u32(smem) + L::O_K + s * L::KV;
-        const uint32_t kd = (uint32_t)__half_as_ushort(__float2half_rn(kdown)) * 0x00010001u;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int t = 8 * m + r, row = 32 * w + t;
-          uint32_t word[J];
-          if (here) lds<J>(raw + t * (D / 2) + c * (D / 8), word);
-#pragma unroll
-          for (int j = 0; j < J; ++j) {
-            uint32_t v[4] = {0, 0, 0, 0};
-            if (here) {
-              uint16_t a;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a) : "r"(sc + (t * NG + j / JG) * 2));
-              // an infinite scale (codes of 0) has to make the logit NaN: 0 * infinity does
-              unpack(word[j], mul_half2((uint32_t)a * 0x00010001u, kd), v);
+          top = __reduce_max_sync(0xffffffffu, top);
+          if (top >= 0x7c00u) {  // scales that stand for NaN: their tokens, group by group
+            if (val) {
+              odd = 1;
+              for (int gr = 0; gr < NG; ++gr) {
+                uint16_t x;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(sc + ((lane >> 1) * NG + gr) * 4 + (lane & 1) * 2));
+                const uint32_t bits = __ballot_sync(0xffffffffu, in && (x & 0x7c00u) == 0x7c00u);
+                if (lane == 0) odds[((g & 3) * UNP + w) * NG + gr] = bits;
+              }
             }
-            const int q8 = 4 * j + c;
-            sts128(k_to + (q8 >> 3) * (TOK * 128) + row * 128 + (((q8 & 7) ^ (row & 7)) << 4), v);
+            top = __reduce_max_sync(0xffffffffu, fine);
           }
+          ex = min(max((int)(top >> 10) - 14, -14), 16);  // the largest scale is at most 2^ex
         }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&kfull[s]);
-        load_k(i + 1, next);
-        // ---- values (zeros outside the sequence and for scales that stand for NaN)
-        if (here) ok = wait(&rawv[w], got & 1, abort_flag);
-        ok = ok && wait(&vempty[s], ((g >> 1) & 1) ^ 1, abort_flag);
+        if (lane == 0) {
+          if (val) {
+            exps[(g & 3) * UNP + w].y = here ? (float)ex : NINF;
+            flag[(g & 3) * UNP + w] = odd;
+          } else {
+            exps[(g & 3) * UNP + w].x = __uint_as_float((uint32_t)(127 + ex) << 23);
+          }
+          mbar_arrive(&xfull[g & 3]);
+        }
+        // 2^-ex in both halves
+        const uint32_t down = (uint32_t)__half_as_ushort(__float2half_rn(__uint_as_float((uint32_t)(127 - ex) << 23))) * 0x00010001u;
+        ok = wait(&empty[s], ((g >> 1) & 1) ^ 1, abort_flag);
         if (!ok) break;
-        const uint32_t v_to = smem_u32(smem) + L::O_V + s * L::KV;
-        const uint32_t vd = (uint32_t)__half_as_ushort(__float2half_rn(vdown)) * 0x00010001u;
+        const uint32_t to0 = smem_u32(smem) + (val ? L::O_V : L::O_K) + s * L::KV + 32 * w * 128;
+        if (!here) {
+          for (int x = lane; x < 32 * D / 8; x += 32) {
+            const uint32_t zero[4] = {0, 0, 0, 0};
+            sts128(to0 + (x >> 8) * (TOK * 128) + (x & 255) * 16, zero);
+          }
+        } else if (!val) {
+          // keys; what stands for tokens outside the sequence gives logits that the softmax masks
+#pragma unroll 2
+          for (int m = 0; m < 4; ++m) {
+            const int t = 8 * m + r;
+            uint32_t word[J], ks[(NG + 1) / 2];  // the token's codes and scales (two to a word)
+            lds<J>(raw + t * (D / 2) + c * (D / 8), word);
+            if constexpr (NG == 1) {
+              uint16_t x;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(sc + t * 2));
+              ks[0] = x;
+            } else {
+              lds<NG / 2>(sc + t * (NG * 2), ks);
+            }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {  // eights of tokens: this lane's are 8 m + 2 c + b
-          uint32_t word[J], scale[NG];  // words: blocks of b = 0, then of b = 1; scales: pairs (b = 0, b = 1)
-          if (here) {
-            lds<J>(raw_v + m * (4 * D) + (r * 4 + c) * (D / 8), word);
-            lds<NG>(sc + 64 * NG + (4 * m + c) * (4 * NG), scale);
+            for (int k = 0; k < (NG + 1) / 2; ++k) ks[k] = mul_half2(ks[k], down);
+            const uint32_t to = to0 + t * 128;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              // (an infinite scale, whose codes are 0, has to make the logit NaN: 0 * infinity does)
+              uint32_t v[4];
+              unpack(word[j], prmt(ks[j / JG / 2], 0, j / JG & 1 ? 0x3232 : 0x1010), v);
+              sts128(to + (j >> 1) * (TOK * 128) + (((4 * (j & 1) + c) ^ r) << 4), v);
+            }
+          }
+        } else {
+          // values; zeros outside the sequence and for scales that stand for NaN
+#pragma unroll 2
+          for (int m = 0; m < 4; ++m) {  // eights of tokens: this lane's are 8 m + 2 c + b
+            uint32_t word[J], scale[NG];  // words: blocks of b = 0, then of b = 1; scales: pairs (b = 0, b = 1)
+            lds<J>(raw + m * (4 * D) + (r * 4 + c) * (D / 8), word);
+            lds<NG>(sc + (4 * m + c) * (4 * NG), scale);
             const int t = tok + 8 * m + 2 * c;
             const uint32_t keep = (t >= low && t < high ? 0xffffu : 0u) | (t + 1 >= low && t + 1 < high ? 0xffff0000u : 0u);
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) scale[gr] = mul_half2(scale[gr] & keep & ~odd_halves(scale[gr]), vd);
-          }
+            for (int gr = 0; gr < NG; ++gr) scale[gr] = mul_half2(scale[gr] & keep & (odd ? ~odd_halves(scale[gr]) : ~0u), down);
 #pragma unroll
-          for (int bb = 0; bb < 2; ++bb) {
-            const int row = 32 * w + 8 * m + 2 * c + bb;
+            for (int bb = 0; bb < 2; ++bb) {
+              const uint32_t to = to0 + (8 * m + 2 * c + bb) * 128 + ((r ^ (2 * c + bb)) << 4);
 #pragma unroll
-            for (int jj = 0; jj < J / 2; ++jj) {
-              uint32_t v[4] = {0, 0, 0, 0};
-              if (here) {
+              for (int jj = 0; jj < J / 2; ++jj) {
                 // lower halves are block 2 jj, upper ones 2 jj + 1
-                const uint32_t s2 = prmt(scale[2 * jj / JG], scale[(2 * jj + 1) / JG], bb ? 0x7632 : 0x5410);
-                unpack(word[bb * (J / 2) + jj], s2, v);
+                uint32_t v[4];
+                unpack(word[bb * (J / 2) + jj], prmt(scale[2 * jj / JG], scale[(2 * jj + 1) / JG], bb ? 0x7632 : 0x5410), v);
+                sts128(to + jj * (TOK * 128), v);
               }
-              sts128(v_to + jj * (TOK * 128) + row * 128 + ((r ^ (row & 7)) << 4), v);
             }
           }
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&vfull[s]);
-        load_v(next);
+        if (lane == 0) mbar_arrive(&full[s]);
+        load(i + 1, next);
         got += here;
         at = next;
       }
       if (!ok) {  // copies that are still in flight get their time before the memory is given up
-        const unsigned long long limit = WAIT_NS;
         unsigned long long t0, now;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
         do asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        while (now - t0 < limit / 100);
+        while (now - t0 < WAIT_NS / 100);
       }
     } else {
       // ======================= MMA issue

@@ -143,7 +143,7 @@ def attention_bound(q, keys, values, lens, cu, *, scale: float, causal: bool = T
     * the query, to binary16 after an exact power-of-two scaling: 2^-11 of each coordinate (a coordinate
       below 2^-28 of the row's largest: 2^-39 of that, absorbed), and fp32 sums, (D + 8) 2^-23 of their
       terms' magnitudes (code offsets included: |q| 15 s against |q| 7 s); so a logit is off by at most
-      d = scale sum |q| |k'| (2^-11 + (D + 8) 2^-23), |k'| = |k| + 8 s <= 16 s.
+      d = |scale| sum |q| |k'| (2^-11 + (D + 8) 2^-23), |k'| = |k| + 8 s <= 16 s.
     * a probability: relative exp(2 d) - 1 for d on both sides of the division, 2^-11 to binary16, 2^-11
       for its product with the value scale, 2^-20 for exp2 and the joins
     * fp32 sums over the tokens, of terms of up to 16 value scales: (n / 16 + D + 16) 2^-22
@@ -176,7 +176,7 @@ def attention_bound(q, keys, values, lens, cu, *, scale: float, causal: bool = T
             aq = np.abs(q[row, h])
             # 16 scales of a group are at most 16 / 7 of its largest value (its code is 7), so of the token's
             kmax = k.max(1, keepdims=True) * (16.0 / 7.0) * 1.001
-            d = scale * (k @ aq * 2.0 ** -11 + (kmax * aq).sum(1) * (D + 8) * 2.0 ** -23)
+            d = abs(scale) * (k @ aq * 2.0 ** -11 + (kmax * aq).sum(1) * (D + 8) * 2.0 ** -23)
             rel = np.expm1(2 * d.max() + 2 * d) + 2 * 2.0 ** -11 + 2.0 ** -20
             vmax = np.nanmax(v, 1, keepdims=True, initial=0.0) * (16.0 / 7.0) * 1.001
             e = (p * rel) @ v + np.broadcast_to((p @ vmax) * (n / 16 + D + 16) * 2.0 ** -22, (D,))

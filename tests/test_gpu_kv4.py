@@ -486,3 +486,101 @@ def test_a_layer_from_activations_to_output(lib):
     rel = (a.float() - b.float()).norm() / b.float().norm()
     assert rel < 0.05, float(rel)
     lib.check_device()
+
+
+# ----------------------------------------------------------------------------- many rows to a key head
+
+@pytest.mark.parametrize("D,G", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("rotate", [True, False])
+@pytest.mark.parametrize("window", [0, 90])
+def test_attention_many_rows(lib, D, G, rotate, window):
+    """Row tiles that are full, half empty and missing, sequences from one token on, several row chunks and steps."""
+    sc = Scene([700, 1, 129, 40, 300], [300, 1, 128, 40, 0], heads=1, D=D, G=G, page=64, rotate=rotate, seed=D + G + window)
+    q = sc.queries(2)
+    got = lib.kv4_attention(dev(q, True), sc.cache(lib), *sc.where(), max_new=300, max_len=700, window=window)
+    sc.check_attention(host(got), q, window=window)
+    got = lib.kv4_attention(dev(q), sc.cache(lib), *sc.where(), max_new=300, max_len=700, window=window, scale=-0.05)
+    sc.check_attention(host(got), q, window=window, scale=-0.05)
+    lib.check_device()
+
+
+@pytest.mark.parametrize("k_scale,v_scale,std", [(1e4, 1.0, 1e-4), (1e-5, 1e-5, 1e4), (1.0, 6e4, 1.0), (1.0, 2e5, 1.0),
+                                                 (1.0, 1e-6, 1.0), (0.0, 1.0, 1.0), (1.0, 0.0, 0.0), (8.0, 30.0, 8.0)])
+def test_attention_many_rows_magnitudes(lib, k_scale, v_scale, std):
+    """As test_attention_magnitudes (at 2e5 some groups overflow their scale and stand for NaN)."""
+    sc = Scene([150, 200], [150, 60], heads=1, D=64, G=32, k_scale=k_scale, v_scale=v_scale, rotate=False, outliers=False)
+    q = sc.queries(3, std=std)
+    got = lib.kv4_attention(dev(q), sc.cache(lib), *sc.where(), max_new=150, max_len=200)
+    sc.check_attention(host(got), q)
+
+
+def test_attention_many_rows_scales_apart(lib):
+    """Value scales that grow by 2^12 along the sequence, and from group to group."""
+    sc = Scene([400], [130], heads=1, D=128, G=32, rotate=False, outliers=False)
+    sc.v = [sc.bf16(sc.v[0] * 2.0 ** (np.arange(400) / 32)[:, None, None] * np.repeat(2.0 ** np.arange(0, 12, 3), 32))]
+    sc._quantise()
+    q = sc.queries(2, std=0.1)
+    got = lib.kv4_attention(dev(q), sc.cache(lib), *sc.where(), max_new=130, max_len=400)
+    sc.check_attention(host(got), q)
+
+
+def test_many_rows_nan_reaches_only_rows_that_see_it(lib):
+    for which, value in ((0, np.nan), (1, np.nan), (1, np.inf)):
+        sc = Scene([300], [200], heads=1, D=64, G=32, rotate=False)
+        q = sc.queries(2)
+        cache = sc.cache(lib, held=[100])
+        rows = [sc.rows(sc.k), sc.rows(sc.v)]
+        rows[which][72, 0, 5] = value         # position 172
+        lib.kv4_append(cache, dev(rows[0]), dev(rows[1]), *sc.where())
+        for window in (0, 50):
+            got = host(lib.kv4_attention(dev(q), cache, *sc.where(), max_new=200, max_len=300, window=window))
+            kw = dict(scale=64 ** -0.5, window=window)
+            ref = O.attention(q, sc.keys, sc.values, sc.lens, sc.cu, **kw)
+            bound = O.attention_bound(q, sc.keys, sc.values, sc.lens, sc.cu, **kw)
+            sees = np.zeros(sc.T, bool)
+            sees[72:(72 + window if window else 200)] = True
+            ok = np.abs(got - ref) <= bound + (np.abs(ref) + bound) * 2.0 ** -8
+            assert ok[~sees].all()
+            if which == 0:
+                assert np.isnan(got[sees]).all()
+            else:
+                assert np.isnan(got[sees][:, :, :32]).all() and ok[sees][:, :, 32:].all()
+
+
+def test_many_rows_pages_outside_the_cache(lib):
+    sc = Scene([600, 70], [150, 70], heads=2, D=64, G=32, page=32)
+    cache = sc.cache(lib)
+    table, lens, cu = sc.where()
+    q = sc.queries(2)
+    lib.check_device()
+    t = table.clone()
+    t[0, 2], t[0, 9], t[1, 1] = -1, sc.pages, 2 ** 31 - 1
+    got = lib.kv4_attention(dev(q, True), cache, t, lens, cu, max_new=150, max_len=600)
+    with pytest.raises(lib.RotError) as e:
+        lib.check_device()
+    assert e.value.status == lib.ROT_EINVAL
+    gone = [np.zeros(600, bool), np.zeros(70, bool)]
+    gone[0][64:96] = gone[0][288:320] = gone[1][32:64] = True
+    sc.check_attention(host(got), q, absent=gone)
+    lib.check_device()
+
+
+def test_many_rows_split_and_left_alone(lib):
+    """A length split over CTAs; launch sizes that name too few rows; rows behind the last sequence."""
+    import torch
+    sc = Scene([3000, 70], [70, 20], heads=1, D=128, G=32, page=64)
+    cache = sc.cache(lib)
+    table, lens, cu = sc.where()
+    q = np.concatenate([sc.queries(2), np.ones((5, 2, 128))])
+    out = torch.full((95, 2, 128), -3.0, dtype=torch.bfloat16, device="cuda")
+    assert lib.kv4_attention_workspace(cache, 2, 95, 2, max_new=70, max_len=3000) > 0
+    lib.kv4_attention(dev(q, True), cache, table, lens, cu, max_new=70, max_len=3000, out=out)
+    sc.check_attention(host(out[:90]), q[:90])
+    assert (out[90:] == -3).all()
+    sc = Scene([900, 70], [800, 20], heads=1, D=64, G=64, page=64)
+    q = sc.queries(1)
+    got = lib.kv4_attention(dev(q, True), sc.cache(lib), *sc.where(), max_new=70, max_len=100)
+    sc.check_attention(host(got), q)
+    got = lib.kv4_attention(dev(q, True), sc.cache(lib), *sc.where(), max_new=800, max_len=900, causal=False)
+    sc.check_attention(host(got), q, causal=False)
+    lib.check_device()
