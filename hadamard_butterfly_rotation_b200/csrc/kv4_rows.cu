@@ -152,28 +152,26 @@ __device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lead, uint32_t
 constexpr uint32_t idesc(int n, bool b_n_major) {
   return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(e));
-  return e != 0;
-}
-// (by one thread)
+// Issued by the whole, converged warp; elect.sync picks the lane that does, so that operands stay uniform.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(id), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&w)[4]) {
@@ -678,15 +676,12 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         ok = ok && wait(&pfull[q], g & 1, abort_flag) && wait(&vfull[s], (g >> 1) & 1, abort_flag);
         if (!ok) return;
         tc_after();
-        if (elect_one()) {
+        const uint64_t v_desc = desc(v_at + s * L::KV, TOK * 128, 1024);
 #pragma unroll
-          for (int k = 0; k < TOK / 16; ++k)
-            mma_ts(tmem + 256 + q * D, tmem + q * 128 + 8 * k, desc(v_at + s * L::KV + k * 2048, TOK * 128, 1024), idesc(D, true),
-                   i > 0 || k > 0);
-          commit(&odone[q]);
-          if (last_q) commit(&vempty[s]);
-        }
-        __syncwarp();
+        for (int k = 0; k < TOK / 16; ++k)
+          mma_ts(tmem + 256 + q * D, tmem + q * 128 + 8 * k, v_desc + (k * 2048 >> 4), idesc(D, true), i > 0 || k > 0);
+        commit(&odone[q]);
+        if (last_q) commit(&vempty[s]);
       };
       for (int i = 0; i < n && ok; ++i) {
         const uint32_t g = step + i, s = g & 1;
@@ -695,15 +690,15 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
           if (i > 0) pv(q, i - 1, q == tiles_q - 1);
           if (!ok) break;
           tc_after();
-          if (elect_one()) {
+          // (advancing a descriptor adds to its start address: no carry, shared addresses stay below 2^18)
+          const uint64_t q_desc = desc(q_at + q * (128 * D * 2), 16, 1024), k_desc = desc(k_at + s * L::KV, 16, 1024);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_ss(tmem + q * 128, desc(q_at + q * (128 * D * 2) + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
-                     desc(k_at + s * L::KV + (k >> 2) * (TOK * 128) + (k & 3) * 32, 16, 1024), idesc(TOK, false), k > 0);
-            commit(&sfull[q]);
-            if (q == tiles_q - 1) commit(&kempty[s]);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t ahead = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+            mma_ss(tmem + q * 128, q_desc + ahead, k_desc + ahead, idesc(TOK, false), k > 0);
           }
-          __syncwarp();
+          commit(&sfull[q]);
+          if (q == tiles_q - 1) commit(&kempty[s]);
         }
       }
       for (int q = 0; q < tiles_q && n > 0; ++q) pv(q, n - 1, q == tiles_q - 1);
