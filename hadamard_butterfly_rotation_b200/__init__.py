@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import os
+import struct
 
 import numpy as np
 
@@ -67,7 +68,14 @@ class _KV4SeqsStruct(C.Structure):
                 ("B", _int), ("T", _i64)]
 
 
-_kvc, _kvs = C.POINTER(_KV4CacheStruct), C.POINTER(_KV4SeqsStruct)
+# rot_kv4_cache and rot_kv4_seqs as bytes: a call in a decoding step is mostly this file's time, and a packed
+# string is passed in half the time that a ctypes structure takes to build
+_kv4_cache_pack = struct.Struct("@PqqiiiiPP").pack
+_kv4_seqs_pack = struct.Struct("@PqiPPiq").pack
+assert struct.calcsize("@PqqiiiiPP") == C.sizeof(_KV4CacheStruct) and struct.calcsize("@PqiPPiq") == C.sizeof(_KV4SeqsStruct)
+
+
+_kvc = _kvs = _vp
 _lib.kv4_append.argtypes = [_kvc, _kvs, _vp, _i64, _i64, _vp, _i64, _i64, _int, _vp]
 _lib.kv4_read.argtypes = [_kvc, _kvs, _int, _vp, _vp, _int, _vp]
 _lib.kv4_attention_workspace.argtypes = [_kvc, _int, _i64, _int, _int, _i64, _i64, C.POINTER(C.c_size_t)]
@@ -510,8 +518,7 @@ class KV4Cache:
         self.pages, self.heads, self.page = data.shape[0], data.shape[1], data.shape[2] * 32
         self.k_plan, self.v_plan = k_plan, v_plan
         dense = data.shape[1] * data.shape[2] * data.shape[3]
-        self._c = _KV4CacheStruct(data.data_ptr(), data.stride(0) if data.shape[0] > 1 else dense, self.pages,
-                                  self.page, self.heads, D, G, None, None)
+        self._shape = (data.data_ptr(), data.stride(0) if data.shape[0] > 1 else dense, self.pages, self.page, self.heads, D, G)
 
     @staticmethod
     def tile_bytes(D: int, G: int) -> int:
@@ -533,28 +540,25 @@ class KV4Cache:
         index = self.data.get_device()
         if index < 0:
             raise RotError(ROT_EINVAL, f"the cache must be on a CUDA device, not {self.data.device}")
-        _check_device(index, torch.cuda.current_device(), "the cache")
-        c = self._c
-        for name, plan in (("k_plan", self.k_plan), ("v_plan", self.v_plan)):
-            if plan is None:
-                setattr(c, name, None)
-            elif not plan.handle.value:
-                raise RotError(ROT_EINVAL, f"the cache's {name} was closed")
-            else:
-                setattr(c, name, plan.handle.value)
-        return C.byref(c), index
+        if index != torch.cuda.current_device():
+            _check_device(index, torch.cuda.current_device(), "the cache")
+        k, v = self.k_plan, self.v_plan
+        if (k is not None and not k._h.value) or (v is not None and not v._h.value):
+            raise RotError(ROT_EINVAL, "a plan of the cache was closed")
+        return _kv4_cache_pack(*self._shape, k._h.value if k is not None else 0, v._h.value if v is not None else 0), index
 
 
 def _kv4_on(t, name: str, index: int):
     """A torch tensor on the device of that index, which is the current one (see _arg)."""
     import torch
-    if not isinstance(t, torch.Tensor):
-        raise RotError(ROT_EINVAL, f"{name} must be a torch tensor")
-    at = t.get_device()
-    if at != index:
+    if isinstance(t, torch.Tensor):
+        at = t.get_device()
+        if at == index:
+            return
         if at < 0:
             raise RotError(ROT_EINVAL, f"{name} must be on a CUDA device, not {t.device}")
         _check_device(at, index, name)
+    raise RotError(ROT_EINVAL, f"{name} must be a torch tensor")
 
 
 def _kv4_seqs(table, lens, cu, T: int, index: int):
@@ -572,7 +576,7 @@ def _kv4_seqs(table, lens, cu, T: int, index: int):
     step, unit = table.stride()
     if cols > 1 and unit != 1:
         raise RotError(ROT_EINVAL, "table must have unit stride along its rows")
-    pc = None
+    pc = 0
     if cu is not None:
         _kv4_on(cu, "cu", index)
         if cu.dim() != 1 or cu.shape[0] != B + 1 or cu.dtype != i32 or not cu.is_contiguous():
@@ -580,7 +584,7 @@ def _kv4_seqs(table, lens, cu, T: int, index: int):
         pc = cu.data_ptr()
     elif T != B:
         raise RotError(ROT_EINVAL, f"without cu there is one new token per sequence: got {T} rows for {B} sequences")
-    return C.byref(_KV4SeqsStruct(table.data_ptr(), step if B > 1 and step > cols else cols, cols, lens.data_ptr(), pc, B, T))
+    return _kv4_seqs_pack(table.data_ptr(), step if B > 1 and step > cols else cols, cols, lens.data_ptr(), pc, B, T)
 
 
 def _kv4_rows(t, name: str, heads, D: int, index: int):
@@ -651,14 +655,17 @@ def kv4_read(cache: KV4Cache, table, lens, cu=None, *, total=None, inverse: bool
     T = int(total) if total is not None else lens.shape[0]
     shape = (T, cache.heads, cache.D)
     if out is None:
-        both = _kv4_empty((2, *shape), out_dtype or torch.bfloat16, cache.data.device, stream)
-        k, v = both.unbind(0)
+        kind = out_dtype or torch.bfloat16
+        if kind is not torch.bfloat16 and kind is not torch.float32:
+            raise RotError(ROT_EINVAL, f"out_dtype must be bf16 or fp32, got {kind}")
+        k, v = _kv4_empty(shape, kind, cache.data.device, stream), _kv4_empty(shape, kind, cache.data.device, stream)
+        pk, pv = k.data_ptr(), v.data_ptr()
     else:
         k, v = out
-    pk = _kv4_out(k, "out[0]", (torch.float32, torch.bfloat16), shape, index)
-    pv = _kv4_out(v, "out[1]", (k.dtype,), shape, index)
+        pk = _kv4_out(k, "out[0]", (torch.float32, torch.bfloat16), shape, index)
+        pv = _kv4_out(v, "out[1]", (k.dtype,), shape, index)
     ss = _kv4_seqs(table, lens, cu, T, index)
-    _check(_lib.kv4_read(cs, ss, int(inverse), pk, pv, _dtype_code(k), _kv4_stream(stream, index)))
+    _check(_lib.kv4_read(cs, ss, inverse, pk, pv, _dtype_code(k), _kv4_stream(stream, index)))
     return k, v
 
 
@@ -666,9 +673,9 @@ def kv4_read(cache: KV4Cache, table, lens, cu=None, *, total=None, inverse: bool
 def _kv4_workspace_bytes(shape, index: int, B: int, T: int, Hq: int, window: int, max_new: int, max_len: int) -> int:
     """kv4_attention_workspace of a cache's shape (D, G, heads) on a device: a function of these numbers alone."""
     D, G, heads = shape
-    c = _KV4CacheStruct(None, heads * KV4Cache.tile_bytes(D, G), 0, 32, heads, D, G, None, None)
+    c = _kv4_cache_pack(0, heads * KV4Cache.tile_bytes(D, G), 0, 32, heads, D, G, 0, 0)
     n = C.c_size_t()
-    _check(_lib.kv4_attention_workspace(C.byref(c), B, T, Hq, window, max_new, max_len, C.byref(n)))
+    _check(_lib.kv4_attention_workspace(c, B, T, Hq, window, max_new, max_len, C.byref(n)))
     return int(n.value)
 
 
@@ -700,7 +707,9 @@ def kv4_attention(q, cache: KV4Cache, table, lens, cu=None, *, max_new=None, max
     shape = (T, Hq, D)
     if out is None:
         out = _kv4_empty(shape, torch.bfloat16, q.device, stream)
-    po = _kv4_out(out, "out", (torch.bfloat16,), shape, index)
+        po = out.data_ptr()
+    else:
+        po = _kv4_out(out, "out", (torch.bfloat16,), shape, index)
     pw, nw = None, 0
     if workspace is not None:
         _kv4_on(workspace, "workspace", index)
@@ -723,7 +732,7 @@ def kv4_slot(cache: KV4Cache, table, lens, cu, row: int, head: int, *, total=Non
     ss = _KV4SeqsStruct(tb.ctypes.data, tb.shape[1], tb.shape[1], ln.ctypes.data, c.ctypes.data if c is not None else None,
                         ln.size, ln.size if total is None else int(total))
     out = (_i64 * 3)()
-    _check(_lib.kv4_slot(C.byref(cache._c), C.byref(ss), int(row), int(head), out))
+    _check(_lib.kv4_slot(_kv4_cache_pack(*cache._shape, 0, 0), C.byref(ss), int(row), int(head), out))
     return tuple(int(x) for x in out)
 
 

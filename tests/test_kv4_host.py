@@ -140,7 +140,7 @@ def test_slot_offsets_pass_32_bits(lib):
     """A page far into a large cache: the offset is 64-bit arithmetic (no memory is touched)."""
     tb = lib.KV4Cache.tile_bytes(128, 32)
     cache = lib.KV4Cache.__new__(lib.KV4Cache)
-    cache._c = lib._KV4CacheStruct(None, 16 * tb, 3_000_000, 64, 8, 128, 32, None, None)
+    cache._shape = (0, 16 * tb, 3_000_000, 64, 8, 128, 32)
     seq, pos, at = lib.kv4_slot(cache, [[2_999_999]], [64], None, 0, 7)
     assert at == (2_999_999 * 16 + 15) * tb and at > 2 ** 37
 
