@@ -139,6 +139,75 @@ __device__ __forceinline__ uint32_t kv4_pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+
+// A row spread over four lanes l: value x of the D / 4 of a lane is coordinate 32 (x / 8) + 8 l + x % 8.
+constexpr int KV4_LANES = 4;
+__device__ __forceinline__ int kv4_coordinate(int l, int x) { return 32 * (x / 8) + 8 * l + x % 8; }
+
+// ... as they stand in memory: W words to the block of eight
+template <int D, bool F32>
+struct Kv4Row {
+  static constexpr int W = F32 ? 8 : 4;
+  uint32_t w[D / 32][W];
+  __device__ __forceinline__ void load(const void* base, int64_t at, int l) {
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + (at + 32 * j + 8 * l) * (W / 2));
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const uint4 x = __ldg(p + i / 4);
+        w[j][i] = x.x;
+        w[j][i + 1] = x.y;
+        w[j][i + 2] = x.z;
+        w[j][i + 3] = x.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(void* base, int64_t at, int l) const {
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + (at + 32 * j + 8 * l) * (W / 2));
+#pragma unroll
+      for (int i = 0; i < W; i += 4) p[i / 4] = make_uint4(w[j][i], w[j][i + 1], w[j][i + 2], w[j][i + 3]);
+    }
+  }
+  // Signs from the plan's mask, whose word p has those of coordinates 2 p (bit 15) and 2 p + 1 (bit 31). Read
+  // anew for every row: the lines stay in L1, and sixteen registers do not stay taken.
+  __device__ __forceinline__ void flip(const uint32_t* signs, int l) {
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(signs + 16 * j + 4 * l));
+      const uint32_t sign[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (F32) {
+          w[j][2 * i] ^= (sign[i] << 16) & 0x80000000u;
+          w[j][2 * i + 1] ^= sign[i] & 0x80000000u;
+        } else {
+          w[j][i] ^= sign[i] & 0x80008000u;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void to_float(float (&v)[D / 4]) const {
+#pragma unroll
+    for (int x = 0; x < D / 4; ++x) {
+      if constexpr (F32) v[x] = __uint_as_float(w[x / 8][x % 8]);
+      else v[x] = __uint_as_float(x % 2 ? w[x / 8][x % 8 / 2] & 0xffff0000u : w[x / 8][x % 8 / 2] << 16);
+    }
+  }
+  __device__ __forceinline__ void from_float(const float (&v)[D / 4]) {
+#pragma unroll
+    for (int x = 0; x < D / 4; x += 2) {
+      if constexpr (F32) {
+        w[x / 8][x % 8] = __float_as_uint(v[x]);
+        w[x / 8][x % 8 + 1] = __float_as_uint(v[x + 1]);
+      } else {
+        w[x / 8][x % 8 / 2] = kv4_pack_bf16(v[x], v[x + 1]);
+      }
+    }
+  }
+};
 #endif
 
 // launchers: arguments already checked (kv4_api.cu)

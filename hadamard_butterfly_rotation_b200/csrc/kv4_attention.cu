@@ -787,14 +787,14 @@ Kv4Split kv4_split(int D, int B, int heads, int share, int window, int64_t max_n
   sp.rows = sp.many ? KV4_ROWS : rows > 8 && D < 256 ? 16 : 8;
   sp.chunks = (int)std::min<int64_t>(std::max<int64_t>((rows + sp.rows - 1) / sp.rows, 1), 1 << 20);
   if (sp.many) {
-    // one CTA to an SM: the number of parts that wastes least of the last round, a CTA's start and end counted
-    // as three steps of 128 tokens
+    // one CTA to an SM: the number of parts that wastes least of the last round, a CTA's start and end, and the
+    // parts' way through memory, counted as seven steps (a split by four of 64 steps each measured 391 us against 347) of 128 tokens
     const int64_t units = std::max<int64_t>((int64_t)B * heads * sp.chunks, 1), steps = std::max<int64_t>((max_len + 127) / 128, 1);
     double best = 0.0;
     sp.splits = 1;
     for (int64_t n = 1; n <= 16 && n <= std::max<int64_t>(steps / 4, 1); ++n) {
       const int64_t rounds = (units * n + sms - 1) / sms;
-      const double use = (double)(units * steps) / (double)(rounds * sms * ((steps + n - 1) / n + 3));
+      const double use = (double)(units * steps) / (double)(rounds * sms * ((steps + n - 1) / n + 7));
       if (use > best * 1.02) {
         best = use;
         sp.splits = (int)n;

@@ -20,75 +20,6 @@ constexpr int CTA = 128;  // two warps for keys, two for values
 constexpr int append_ctas(int D) { return D == 256 ? 2 : 4; }
 constexpr int read_ctas(int D) { return D == 256 ? 2 : 6; }
 
-// A lane's coordinates of a row: value x of N is coordinate 32 (x / 8) + 8 l + x % 8.
-constexpr int LANES = 4;
-__device__ __forceinline__ int coordinate(int l, int x) { return 32 * (x / 8) + 8 * l + x % 8; }
-
-// ... as they stand in memory: W words to the block of eight
-template <int D, bool F32>
-struct Raw {
-  static constexpr int W = F32 ? 8 : 4;
-  uint32_t w[D / 32][W];
-  __device__ __forceinline__ void load(const void* base, int64_t at, int l) {
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + (at + 32 * j + 8 * l) * (W / 2));
-#pragma unroll
-      for (int i = 0; i < W; i += 4) {
-        const uint4 x = __ldg(p + i / 4);
-        w[j][i] = x.x;
-        w[j][i + 1] = x.y;
-        w[j][i + 2] = x.z;
-        w[j][i + 3] = x.w;
-      }
-    }
-  }
-  __device__ __forceinline__ void store(void* base, int64_t at, int l) const {
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + (at + 32 * j + 8 * l) * (W / 2));
-#pragma unroll
-      for (int i = 0; i < W; i += 4) p[i / 4] = make_uint4(w[j][i], w[j][i + 1], w[j][i + 2], w[j][i + 3]);
-    }
-  }
-  // Signs from the plan's mask, whose word p has those of coordinates 2 p (bit 15) and 2 p + 1 (bit 31). Read
-  // anew for every row: the lines stay in L1, and sixteen registers do not stay taken.
-  __device__ __forceinline__ void flip(const uint32_t* signs, int l) {
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(signs + 16 * j + 4 * l));
-      const uint32_t sign[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (F32) {
-          w[j][2 * i] ^= (sign[i] << 16) & 0x80000000u;
-          w[j][2 * i + 1] ^= sign[i] & 0x80000000u;
-        } else {
-          w[j][i] ^= sign[i] & 0x80008000u;
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ void to_float(float (&v)[D / 4]) const {
-#pragma unroll
-    for (int x = 0; x < D / 4; ++x) {
-      if constexpr (F32) v[x] = __uint_as_float(w[x / 8][x % 8]);
-      else v[x] = __uint_as_float(x % 2 ? w[x / 8][x % 8 / 2] & 0xffff0000u : w[x / 8][x % 8 / 2] << 16);
-    }
-  }
-  __device__ __forceinline__ void from_float(const float (&v)[D / 4]) {
-#pragma unroll
-    for (int x = 0; x < D / 4; x += 2) {
-      if constexpr (F32) {
-        w[x / 8][x % 8] = __float_as_uint(v[x]);
-        w[x / 8][x % 8 + 1] = __float_as_uint(v[x + 1]);
-      } else {
-        w[x / 8][x % 8 / 2] = kv4_pack_bf16(v[x], v[x + 1]);
-      }
-    }
-  }
-};
-
 // The lane's codes of token t in its tile, word j block j's eight: a key has them in one piece of D / 8 bytes,
 // a value in two of D / 16 whose halfwords are block j's lower and upper four.
 template <int D>
@@ -212,16 +143,16 @@ __device__ __forceinline__ uint32_t decide(float y, float s) {
 // about 1e-3; more where the row's largest value is far above the group's) are taken again from a 64-bit
 // sum of their own, by the whole warp. A code that flips moves its value by a whole step, which no
 // tolerance on the value can tell from a mistake. A group that holds a NaN, or whose scale overflows,
-// keeps that scale and codes of 0. Lane l of a row works out the scales of the groups g = l mod LANES and
-// returns them in scale[g / LANES]; w: the codes, block by block. All lanes of the warp enter.
+// keeps that scale and codes of 0. Lane l of a row works out the scales of the groups g = l mod KV4_LANES and
+// returns them in scale[g / KV4_LANES]; w: the codes, block by block. All lanes of the warp enter.
 template <int D, int NG, bool F32>
 __device__ __forceinline__ void quantise(const float (&z)[D / 4], bool rot, float norm, const void* base, int64_t at,
                                          const uint32_t* sign, int lane, uint32_t (&w)[D / 32],
-                                         uint16_t (&scale)[(NG + LANES - 1) / LANES]) {
+                                         uint16_t (&scale)[(NG + KV4_LANES - 1) / KV4_LANES]) {
   constexpr int N = D / 4;
   constexpr int M = N / NG;                                 // the lane's coordinates of a group
-  constexpr int OWN = (NG + LANES - 1) / LANES;          // groups whose scales the lane works out
-  const int l = lane % LANES;
+  constexpr int OWN = (NG + KV4_LANES - 1) / KV4_LANES;          // groups whose scales the lane works out
+  const int l = lane % KV4_LANES;
   const float n1 = rot ? norm : 1.0f;
   float m[NG], row = 0.0f;
 #pragma unroll
@@ -230,7 +161,7 @@ __device__ __forceinline__ void quantise(const float (&z)[D / 4], bool rot, floa
 #pragma unroll
     for (int i = 1; i < M; ++i) m[g] = kv4_max_nan(m[g], fabsf(z[g * M + i]));
 #pragma unroll
-    for (int x = 1; x < LANES; x *= 2) m[g] = kv4_max_nan(m[g], __shfl_xor_sync(0xffffffffu, m[g], x));
+    for (int x = 1; x < KV4_LANES; x *= 2) m[g] = kv4_max_nan(m[g], __shfl_xor_sync(0xffffffffu, m[g], x));
     row = fmaxf(row, m[g]);
   }
   // exact values of the marked coordinates (of 32 from x0 on) of every lane
@@ -240,7 +171,7 @@ __device__ __forceinline__ void quantise(const float (&z)[D / 4], bool rot, floa
       const int src = __ffs(left) - 1;
       const int i = __shfl_sync(0xffffffffu, __ffs(mask) - 1, src);
       const double y = exact_coordinate<D, F32>(base, __shfl_sync(0xffffffffu, at, src), sign,
-                                                coordinate(src % LANES, x0 + i), lane);
+                                                kv4_coordinate(src % KV4_LANES, x0 + i), lane);
       if (lane == src) {
         mask &= mask - 1;
         take(i, y);
@@ -255,7 +186,7 @@ __device__ __forceinline__ void quantise(const float (&z)[D / 4], bool rot, floa
     float mine = m[0];
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-      if (g / LANES == k && l == g % LANES) mine = m[g];
+      if (g / KV4_LANES == k && l == g % KV4_LANES) mine = m[g];
     // the row's largest value over the group's; without a rotation z is exact, only the quotient is not
     far[k] = mine > 0.0f ? (rot ? fminf(__fdividef(row, mine), 1e6f) : 1.0f) : 0.0f;
     q7[k] = __fdiv_rn(mine * n1, 7.0f);
@@ -265,11 +196,11 @@ __device__ __forceinline__ void quantise(const float (&z)[D / 4], bool rot, floa
   if (rot && __any_sync(0xffffffffu, near)) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const bool own = l == g % LANES;
-      const float eps = 4e-7f * far[g / LANES], q = q7[g / LANES];
+      const bool own = l == g % KV4_LANES;
+      const float eps = 4e-7f * far[g / KV4_LANES], q = q7[g / KV4_LANES];
       const bool mine = own && __half_as_ushort(__float2half_rn(q * (1.0f - eps))) != __half_as_ushort(__float2half_rn(q * (1.0f + eps)));
       // (a row's owner lane of the group tells the row's other lanes)
-      const int src = lane / LANES * LANES + g % LANES;
+      const int src = lane / KV4_LANES * KV4_LANES + g % KV4_LANES;
       const bool hit = __shfl_sync(0xffffffffu, (int)mine, src);
       const float least = m[g] * (1.0f - 2.0f * __shfl_sync(0xffffffffu, eps, src));
       if (!__any_sync(0xffffffffu, hit)) continue;
@@ -282,8 +213,8 @@ __device__ __forceinline__ void quantise(const float (&z)[D / 4], bool rot, floa
         candidates(mask, g * M + h, [&](int, double y) { big = fmax(big, fabs(y)); });
       }
 #pragma unroll
-      for (int x = 1; x < LANES; x *= 2) big = fmax(big, __shfl_xor_sync(0xffffffffu, big, x));
-      if (mine) q7[g / LANES] = __fdiv_rn((float)big, 7.0f);
+      for (int x = 1; x < KV4_LANES; x *= 2) big = fmax(big, __shfl_xor_sync(0xffffffffu, big, x));
+      if (mine) q7[g / KV4_LANES] = __fdiv_rn((float)big, 7.0f);
     }
   }
   float f[OWN], border[OWN];
@@ -304,8 +235,8 @@ __device__ __forceinline__ void quantise(const float (&z)[D / 4], bool rot, floa
   bool again = false;
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    const int src = lane / LANES * LANES + g % LANES;
-    const float fg = __shfl_sync(0xffffffffu, f[g / LANES], src), bg = __shfl_sync(0xffffffffu, border[g / LANES], src);
+    const int src = lane / KV4_LANES * KV4_LANES + g % KV4_LANES;
+    const float fg = __shfl_sync(0xffffffffu, f[g / KV4_LANES], src), bg = __shfl_sync(0xffffffffu, border[g / KV4_LANES], src);
     float worst = 0.0f;  // distance from the rounded code: a half is the border
 #pragma unroll
     for (int x = g * M; x < (g + 1) * M; x += (M < 8 ? M : 8)) {
@@ -330,9 +261,9 @@ __device__ __forceinline__ void quantise(const float (&z)[D / 4], bool rot, floa
   if (__any_sync(0xffffffffu, again)) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const int src = lane / LANES * LANES + g % LANES;
-      const float fg = __shfl_sync(0xffffffffu, f[g / LANES], src), bg = __shfl_sync(0xffffffffu, border[g / LANES], src);
-      const float s = __half2float(__ushort_as_half((uint16_t)__shfl_sync(0xffffffffu, (int)scale[g / LANES], src)));
+      const int src = lane / KV4_LANES * KV4_LANES + g % KV4_LANES;
+      const float fg = __shfl_sync(0xffffffffu, f[g / KV4_LANES], src), bg = __shfl_sync(0xffffffffu, border[g / KV4_LANES], src);
+      const float s = __half2float(__ushort_as_half((uint16_t)__shfl_sync(0xffffffffu, (int)scale[g / KV4_LANES], src)));
 #pragma unroll
       for (int h = 0; h < M; h += 32) {
         uint32_t mask = 0;
@@ -370,14 +301,14 @@ __global__ void __launch_bounds__(CTA, append_ctas(D)) append_kernel(const __gri
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t row0 = (int64_t)blockIdx.x * 8;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES, i = lane / LANES;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % KV4_LANES, i = lane / KV4_LANES;
   const int h0 = blockIdx.y * span, heads = min(span, c.heads - h0);
   const bool val = warp >= 2, rot = val ? c.v_rot : c.k_rot;
   const int64_t row = row0 + i, head = val ? in.v_head : in.k_head;
   const void* base = val ? in.v : in.k;
   // (lanes behind the last row take row 0's inputs, and store nothing)
   int64_t at = (row < c.T ? row : 0) * (val ? in.v_token : in.k_token) + (h0 + (warp & 1)) * head;
-  Raw<D, F32> raw;
+  Kv4Row<D, F32> raw;
   if ((warp & 1) < heads) raw.load(base, at, l);
   const uint32_t* signs = val ? c.v_sign : c.k_sign;
   find(c, row0, places);
@@ -392,16 +323,16 @@ __global__ void __launch_bounds__(CTA, append_ctas(D)) append_kernel(const __gri
     const int64_t here = at;
     at += 2 * head;
     if (h + 2 < heads) raw.load(base, at, l);
-    if (rot) kv4_fwht<D / 4, LANES>(z, lane);
+    if (rot) kv4_fwht<D / 4, KV4_LANES>(z, lane);
     Codes<D> codes;
-    uint16_t scale[(NG + LANES - 1) / LANES];
+    uint16_t scale[(NG + KV4_LANES - 1) / KV4_LANES];
     quantise<D, NG, F32>(z, rot, norm, base, here, signs, lane, codes.w, scale);
     if (tile >= 0) {
       uint8_t* to = c.data + tile + (int64_t)(h0 + h) * c.tpp * c.tile_bytes;
       codes.store(to, t, l, val);
 #pragma unroll
       for (int g = 0; g < NG; ++g)
-        if (l == g % LANES) *reinterpret_cast<uint16_t*>(to + scale_at<D, NG>(t, g, val)) = scale[g / LANES];
+        if (l == g % KV4_LANES) *reinterpret_cast<uint16_t*>(to + scale_at<D, NG>(t, g, val)) = scale[g / KV4_LANES];
     }
   }
 }
@@ -414,7 +345,7 @@ __global__ void __launch_bounds__(CTA, read_ctas(D)) read_kernel(const __grid_co
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t row0 = (int64_t)blockIdx.x * 8;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LANES, i = lane / LANES;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % KV4_LANES, i = lane / KV4_LANES;
   const int h0 = blockIdx.y * span, heads = min(span, c.heads - h0);
   const bool val = warp >= 2, rot = inverse && (val ? c.v_rot : c.k_rot);
   const uint32_t* signs = val ? c.v_sign : c.k_sign;
@@ -461,8 +392,8 @@ __global__ void __launch_bounds__(CTA, read_ctas(D)) read_kernel(const __grid_co
       asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(by));
       asm("mov.b64 {%0, %1}, %2;" : "=f"(z[x]), "=f"(z[x + 1]) : "l"(v));
     }
-    Raw<D, F32> raw;
-    if (rot) kv4_fwht<D / 4, LANES>(z, lane);  // T^T = D H / sqrt(D)
+    Kv4Row<D, F32> raw;
+    if (rot) kv4_fwht<D / 4, KV4_LANES>(z, lane);  // T^T = D H / sqrt(D)
     raw.from_float(z);
     if (rot && signs) raw.flip(signs, l);
     if (places.t[i] >= 0) raw.store(const_cast<void*>(val ? out.v : out.k), at, l);

@@ -10,8 +10,8 @@
 //   O += P V     A is P in TMEM, B is V in shared memory as it lies in the cache, tokens by rows of
 //                coordinates (N-major); O stays in TMEM and is rescaled only when a row's reference rises by
 //                more than 2^8
-// Warps 0..7 are the softmax of the two row tiles, 8..11 fetch and unpack keys, 12..15 values (each one cache
-// tile of 32 tokens per step, with a bulk copy of its own in flight), warp 16 issues the MMAs. While one row tile is
+// Warps 0..7 are the softmax of the two row tiles, 8..11 fetch and unpack keys, 12..14 values (a cache tile of
+// 32 tokens at a time in turn, with a bulk copy of its own in flight), warp 15 issues the MMAs. While one row tile is
 // in its softmax, the tensor pipe works on the other. The unpacking is paid once for 256 rows; with keys and values
 // in the same warps a step waited for the values' stage before the next keys could be unpacked.
 // Codes become binary16 values code * scale 2^-e, e the exponent of the largest scale of the 32 tokens, so that
@@ -31,7 +31,11 @@ using namespace kv4;
 __device__ int g_kv4_rows_error = 0;
 
 constexpr int ROWS = KV4_ROWS, TOK = 128;
-constexpr int SOFT = 8, UNP = 4, WARPS = SOFT + 2 * UNP + 1, CTA = 32 * WARPS;
+#ifndef BLKN
+#define BLKN 64
+#endif
+constexpr int BLK = BLKN;  // columns of S that a softmax warp reads at a time
+constexpr int SOFT = 8, UNP = 4, VUNP = 3, WARPS = SOFT + UNP + VUNP + 1, CTA = 32 * WARPS;
 constexpr unsigned long long WAIT_NS = 1000000000ull;
 
 template <int D, int NG>
@@ -43,8 +47,8 @@ struct Lay {
   static constexpr int CODES = 16 * D;                 // packed keys, or values, of a cache tile
   static constexpr int SCALES = 64 * NG;               // their scales
   static constexpr int RAW = CODES + 2 * SCALES;       // an unpacking warp's: codes, two sets of scales
-  static constexpr int O_RAW = O_V + 2 * KV;           // [2 UNP]
-  static constexpr int O_FAC = O_RAW + 2 * UNP * RAW;  // per row: logit factor
+  static constexpr int O_RAW = O_V + 2 * KV;           // [UNP + VUNP]
+  static constexpr int O_FAC = O_RAW + (UNP + VUNP) * RAW;  // per row: logit factor
   static constexpr int O_SEEN = O_FAC + ROWS * 4;      // per row: the tokens that it sees
   static constexpr int O_ML = O_SEEN + ROWS * 8;       // per row: reference and sum at the end
   static constexpr int O_EXP = O_ML + ROWS * 8;        // [4 steps][UNP]: 2^key exponent, value exponent
@@ -112,32 +116,36 @@ __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::befor
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// A warp's 32 lanes by N columns of TMEM, in registers
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 
@@ -209,7 +217,7 @@ __device__ __forceinline__ float2 lds2(uint32_t addr) {
 template <int D, int NG, bool QF32>
 __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Params p) {
   using L = Lay<D, NG>;
-  constexpr int J = D / 32, JG = J / NG, V = D / 32;
+  constexpr int J = D / 32, JG = J / NG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
   uint64_t* sfull = xfull + 4;                                     // [2] S of a row tile -> softmax
   uint64_t* pfull = sfull + 2;                                     // [2] P of a row tile -> MMA
   uint64_t* odone = pfull + 2;                                     // [2] P V of a row tile done -> softmax
-  uint64_t* raws = odone + 2;                                      // [2 UNP] packed keys, then packed values
+  uint64_t* raws = odone + 2;                                      // [UNP + VUNP] packed keys, then packed values
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::O_TMEM);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::O_TMEM + 8);
   float* r_fac = reinterpret_cast<float*>(smem + L::O_FAC);
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
       mbar_init(&odone[s], 1);
     }
     for (int s = 0; s < 4; ++s) mbar_init(&xfull[s], 2 * UNP);
-    for (int s = 0; s < 2 * UNP; ++s) mbar_init(&raws[s], 1);
+    for (int s = 0; s < UNP + VUNP; ++s) mbar_init(&raws[s], 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -286,79 +294,49 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
     const int n = to - from, tok_a = (step_a + from) * TOK;
 
     // ---- query rows: rotate, scale to binary16 by a power of two, K-major
-    constexpr int BATCH = 4;  // rows in flight to a warp
-    for (int r0 = warp * BATCH; r0 < tiles_q * 128; r0 += WARPS * BATCH) {
-      float v[BATCH][V], m[BATCH];
+    // (four lanes to a row, eight rows to a warp)
+    const int l = lane % KV4_LANES;
+    const float row_fac = p.c.k_rot ? p.scale_log2 * p.norm : p.scale_log2;
+    for (int rr = warp * 8 + lane / KV4_LANES; rr < tiles_q * 128; rr += WARPS * 8) {
+      const int row = row0 + rr, token = row / p.share;
+      Kv4Row<D, QF32> raw;
+      if (row < n_rows) {
+        raw.load(p.q, (first + token) * p.q_token + ((int64_t)h * p.share + (row - token * p.share)) * p.q_head, l);
+        if (p.c.k_rot && p.c.k_sign) raw.flip(p.c.k_sign, l);
+      } else {
 #pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        const int row = row0 + r0 + u;
+        for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[u][i] = 0.0f;
+          for (int i = 0; i < Kv4Row<D, QF32>::W; ++i) raw.w[j][i] = 0;
+      }
+      float v[D / 4], m = 0.0f;
+      raw.to_float(v);
+      if (p.c.k_rot) kv4_fwht<D / 4, KV4_LANES>(v, lane);
+#pragma unroll
+      for (int x = 0; x < D / 4; ++x) m = fmaxf(m, fabsf(v[x]));
+#pragma unroll
+      for (int x = 1; x < KV4_LANES; x *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+      const int e = m > 0.0f ? min(max(141 - (int)(__float_as_uint(m) >> 23), -100), 100) : 0;
+      // (a negative softmax scale turns the query around, so that the factor is not negative)
+      const float up = copysignf(__uint_as_float((uint32_t)(127 + e) << 23), row_fac);
+      const uint32_t to = smem_u32(smem) + L::O_Q + (rr >> 7) * (128 * D * 2) + (rr & 127) * 128;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {  // coordinates 32 j + 8 l .., in the order (0, 4) (1, 5) (2, 6) (3, 7)
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack_half(v[8 * j + i] * up, v[8 * j + i + 4] * up);
+        sts128(to + (j >> 1) * (128 * 128) + (((4 * (j & 1) + l) ^ (rr & 7)) << 4), w);
+      }
+      if (l == 0) {
+        // (above zero, so that a masked logit stays -inf: a factor this small makes every logit 0 all the same)
+        r_fac[rr] = fmaxf(fabsf(row_fac) * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
+        int2 seen = make_int2(0, high);  // the tokens that the row sees: [x, y)
         if (row < n_rows) {
-          const int64_t at = (first + row / p.share) * p.q_token + ((int64_t)h * p.share + row % p.share) * p.q_head + lane * V;
-#pragma unroll
-          for (int i = 0; i < V; i += 2) {
-            if constexpr (QF32) {
-              const float2 x = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p.q) + at + i));
-              v[u][i] = x.x;
-              v[u][i + 1] = x.y;
-            } else {
-              const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + at + i));
-              v[u][i] = __uint_as_float(x << 16);
-              v[u][i + 1] = __uint_as_float(x & 0xffff0000u);
-            }
-          }
+          const int pos = pos0 + token;
+          if (p.causal) seen.y = min(high, pos + 1);
+          if (p.window) seen.x = max(0, pos - p.window + 1);
         }
-      }
-      if (p.c.k_rot) {
-        if (p.c.k_sign) {
-#pragma unroll
-          for (int i = 0; i < V; i += 2) {
-            const uint32_t w = __ldg(p.c.k_sign + (lane * V + i) / 2);
-#pragma unroll
-            for (int u = 0; u < BATCH; ++u) {
-              v[u][i] = kv4_signed(v[u][i], w, 0);
-              v[u][i + 1] = kv4_signed(v[u][i + 1], w, 1);
-            }
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u) kv4_fwht<V, 32>(v[u], lane);
-      }
-      const float fac = p.c.k_rot ? p.scale_log2 * p.norm : p.scale_log2;
-#pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        m[u] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) m[u] = fmaxf(m[u], fabsf(v[u][i]));
-      }
-#pragma unroll
-      for (int x = 1; x < 32; x *= 2)
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], x));
-#pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        const int rr = r0 + u, row = row0 + rr;
-        const int e = m[u] > 0.0f ? min(max(141 - (int)(__float_as_uint(m[u]) >> 23), -100), 100) : 0;
-        // (a negative softmax scale turns the query around, so that the factor is not negative)
-        const float up = copysignf(__uint_as_float((uint32_t)(127 + e) << 23), fac);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int d = lane * V + i, q8 = d >> 3, place = 2 * (d & 3) + ((d >> 2) & 1);
-          uint8_t* at = smem + L::O_Q + (rr >> 7) * (128 * D * 2) + (q8 >> 3) * (128 * 128) + (rr & 127) * 128 +
-                        (((q8 & 7) ^ (rr & 7)) << 4) + place * 2;
-          *reinterpret_cast<__half*>(at) = __float2half_rn(v[u][i] * up);
-        }
-        if (lane == 0) {
-          r_fac[rr] = fabsf(fac) * __uint_as_float((uint32_t)(127 - e) << 23);
-          int2 seen = make_int2(0, high);  // the tokens that the row sees: [x, y)
-          if (row < n_rows) {
-            const int pos = pos0 + row / p.share;
-            if (p.causal) seen.y = min(high, pos + 1);
-            if (p.window) seen.x = max(0, pos - p.window + 1);
-          }
-          r_seen[rr] = seen;
-        }
+        r_seen[rr] = seen;
       }
     }
     fence_async();
@@ -381,7 +359,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
           if (!ok) break;
           tc_after();
           const bool edge = __any_sync(0xffffffffu, tok < seen.x || tok + TOK > seen.y);
-          float f[4], shift[4], top = NINF, vtop = vref;  // of the step's four cache tiles
+          float f[4], shift[4], vtop = vref;  // of the step's four cache tiles
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const float2 ex = lds2(smem_u32(exps) + ((g & 3) * UNP + c) * 8);
@@ -389,81 +367,101 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
             shift[c] = ex.y;
             vtop = fmaxf(vtop, ex.y);
           }
-          // ---- a row's largest logit
-          uint32_t s[32];
-          auto masked = [&](uint32_t (&x)[32], int c) {
-            const int lo = seen.x - tok - 32 * c, hi = seen.y - tok - 32 * c;
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (k < lo || k >= hi) x[k] = __float_as_uint(NINF);
-          };
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32(s_at + 32 * c, s);
-            wait_ld();
-            if (edge) masked(s, c);
-            float m = __uint_as_float(s[0]), m2 = __uint_as_float(s[1]);
-#pragma unroll
-            for (int k = 2; k < 32; k += 4) {
-              m = max3f(m, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-              if (k + 2 < 32) m2 = max3f(m2, __uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
-            }
-            if (shift[c] != NINF) top = fmaxf(top, fmaxf(m, m2) * f[c]);  // (f >= 0)
-          }
-          if (__any_sync(0xffffffffu, top > ref + 8.0f || vtop > vref)) {
-            const float now = fmaxf(ref, top);
-            const float down = ref == NINF ? 0.0f : ex2(ref - now);
-            const float down_o = down * ex2(vref - vtop);
-            ref = now;
-            vref = vtop;
-            sum *= down;
-            if (i > 0) {
+          // O, and what stands of this step's P (`done` columns of 32 bits), times factors: where a reference rises
+          auto rescale = [&](float by_o, float by_p, int done) {
+            if (i > 0) {  // once the MMA that adds to O is done (nothing stands there in the first step)
               ok = wait(&odone[q], (g - 1) & 1, abort_flag);
-              if (!ok) break;
+              if (!ok) return;
               tc_after();
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                tmem_ld32(o_at + c, s);
+              for (int c = 0; c < D; c += 16) {
+                uint32_t x[16];
+                tmem_ld(o_at + c, x);
                 wait_ld();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) * down_o);
-                tmem_st32(o_at + c, s);
+                for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * by_o);
+                tmem_st(o_at + c, x);
               }
-              wait_st();
             }
-          }
-          // ---- P 2^(7 + the value exponent over the reference one)
-          const float base = (float)P_SHIFT - fmaxf(ref, -3.0e38f);
+            wait_st();
+            const uint32_t by2 = pack_half(by_p, by_p);
+#pragma unroll 1
+            for (int c = 0; c < done; c += 16) {
+              uint32_t x[16];
+              tmem_ld(s_at + c, x);
+              wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32(s_at + 32 * c, s);
+              for (int k = 0; k < 16; ++k) x[k] = mul_half2(x[k], by2);
+              tmem_st(s_at + c, x);
+            }
+            wait_st();
+          };
+          if (vtop > vref) {  // (the same for every row)
+            rescale(ex2(vref - vtop), 1.0f, 0);
+            vref = vtop;
+          }
+          // ---- BLK columns at a time: the largest logit, the exponentials, P over columns of S that have been read. A
+          // row whose logits pass its reference by 2^8 raises it.
+#pragma unroll
+          for (int c = 0; c < TOK / BLK && ok; ++c) {
+            uint32_t x[BLK];
+            tmem_ld(s_at + BLK * c, x);
             wait_ld();
-            const float up = shift[c] - vref, at = base + up;
-            unsigned long long f2, at2, part = 0;
-            asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f[c]));
-            asm("mov.b64 %0, {%1, %1};" : "=l"(at2) : "f"(at));
+            if (edge) {
+              const int lo = seen.x - tok - BLK * c, hi = seen.y - tok - BLK * c;
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              unsigned long long x;
-              asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(s[k]), "r"(s[k + 1]));
-              asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(x), "l"(f2), "l"(at2));
-              asm("mov.b64 {%0, %1}, %2;" : "=r"(s[k]), "=r"(s[k + 1]) : "l"(x));
+              for (int k = 0; k < BLK; ++k)
+                if (k < lo || k >= hi) x[k] = __float_as_uint(NINF);
             }
-            if (edge) masked(s, c);
-            uint32_t pk[16];
+            float top = NINF;
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const float x = ex2(__uint_as_float(s[k])), y = ex2(__uint_as_float(s[k + 1]));
-              unsigned long long xy;
-              asm("mov.b64 %0, {%1, %2};" : "=l"(xy) : "f"(x), "f"(y));
-              asm("add.rn.f32x2 %0, %1, %2;" : "=l"(part) : "l"(part), "l"(xy));
-              pk[k / 2] = pack_half(x, y);
+            for (int e = 0; e < BLK / 32; ++e) {
+              float m[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) m[k] = __uint_as_float(x[32 * e + k]);
+#pragma unroll
+              for (int k = 4; k < 32; k += 8)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  m[u] = k + 4 < 32 ? max3f(m[u], __uint_as_float(x[32 * e + k + u]), __uint_as_float(x[32 * e + k + 4 + u]))
+                                    : fmaxf(m[u], __uint_as_float(x[32 * e + k + u]));
+              // (f > 0; not of a tile that is not there)
+              if (shift[c * BLK / 32 + e] != NINF) top = fmaxf(top, max3f(m[0], m[1], fmaxf(m[2], m[3])) * f[c * BLK / 32 + e]);
             }
-            float pa, pb;
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(pa), "=f"(pb) : "l"(part));
-            sum = fmaf(pa + pb, ex2(fminf(-up, 100.0f)), sum);
-            tmem_st16(s_at + 16 * c, pk);
+            if (__any_sync(0xffffffffu, top > ref + 8.0f)) {
+              const float now = fmaxf(ref, top), down = ref == NINF ? 0.0f : ex2(ref - now);
+              ref = now;
+              sum *= down;
+              rescale(down, down, c * (BLK / 2));
+            }
+            // P 2^(7 + the tile's value exponent over the reference one)
+            uint32_t pk[BLK / 2];
+#pragma unroll
+            for (int e = 0; e < BLK / 32; ++e) {
+              const float up = shift[c * BLK / 32 + e] - vref, at = (float)P_SHIFT - fmaxf(ref, -3.0e38f) + up;
+              unsigned long long f2, at2, part = 0;
+              asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f[c * BLK / 32 + e]));
+              asm("mov.b64 %0, {%1, %1};" : "=l"(at2) : "f"(at));
+#pragma unroll
+              for (int k = 32 * e; k < 32 * e + 32; k += 2) {
+                unsigned long long z;
+                float z0, z1;
+                asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "r"(x[k]), "r"(x[k + 1]));
+                asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(z) : "l"(z), "l"(f2), "l"(at2));
+                asm("mov.b64 {%0, %1}, %2;" : "=f"(z0), "=f"(z1) : "l"(z));
+                z0 = ex2(z0);
+                z1 = ex2(z1);
+                asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(z0), "f"(z1));
+                asm("add.rn.f32x2 %0, %1, %2;" : "=l"(part) : "l"(part), "l"(z));
+                pk[k / 2] = pack_half(z0, z1);
+              }
+              float pa, pb;
+              asm("mov.b64 {%0, %1}, %2;" : "=f"(pa), "=f"(pb) : "l"(part));
+              sum = fmaf(pa + pb, ex2(fminf(-up, 100.0f)), sum);
+            }
+            tmem_st(s_at + BLK / 2 * c, pk);
           }
+          if (!ok) break;
           // ---- value scales that stand for NaN (rare): their groups, in the rows that see the token
           uint32_t flags[4];
           lds<4>(smem_u32(flag) + (g & 3) * 16, flags);
@@ -494,7 +492,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         for (int c = 0; c < D; c += 32) {
           uint32_t s[32];
           if (n > 0 && ok) {
-            tmem_ld32(o_at + c, s);
+            tmem_ld(o_at + c, s);
             wait_ld();
           } else {
 #pragma unroll
@@ -514,43 +512,44 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         }
         tc_before();
       }
-    } else if (warp < SOFT + 2 * UNP) {
-      // ======================= fetch and unpack: cache tile w of every step, its keys or its values
-      const int w = (warp - SOFT) % UNP, r = lane >> 2, c = lane & 3;
+    } else if (warp < SOFT + UNP + VUNP) {
+      // ======================= fetch and unpack: the keys, or the values, of the steps' cache tiles in turn
+      const int r = lane >> 2, c = lane & 3;
       const bool val = warp >= SOFT + UNP;
+      const int job0 = val ? warp - SOFT - UNP : warp - SOFT, stride = val ? VUNP : UNP;  // job: step 4 + tile of the step
       // packed codes and two sets of scales, the next step's on their way while this one's are in use
       const uint32_t raw = smem_u32(smem) + L::O_RAW + (warp - SOFT) * L::RAW, raw_s = raw + L::CODES;
       uint64_t* rawbar = raws + (warp - SOFT);
       uint64_t *full = val ? vfull : kfull, *empty = val ? vempty : kempty;
-      int64_t my_at = -1;  // the lane's tile out of the next 32 steps
-      auto at_of = [&](int i) -> int64_t {
-        if (i >= n) return -1;
-        if ((i & 31) == 0) {
-          const int mine = i + lane, tok = tok_a + mine * TOK + 32 * w;
+      int64_t my_at = -1;  // the lane's tile out of the next 32 jobs
+      auto at_of = [&](int k) -> int64_t {
+        if (job0 + k * stride >= UNP * n) return -1;
+        if ((k & 31) == 0) {
+          const int job = job0 + (k + lane) * stride, tok = tok_a + job * 32;
           my_at = -1;
-          if (mine < n && tok < high) {
+          if (job < UNP * n && tok < high) {
             my_at = kv4_tile_at(p.c, b, tok >> 5, h);
             if (my_at < 0) atomicExch(&g_kv4_rows_error, (int)ROT_EINVAL);
           }
         }
-        return __shfl_sync(0xffffffffu, my_at, i & 31);
+        return __shfl_sync(0xffffffffu, my_at, k & 31);
       };
-      auto load = [&](int i, int64_t at) {
+      auto load = [&](int k, int64_t at) {
         if (at >= 0 && lane == 0) {
           const uint8_t* from = p.c.data + at;
           mbar_expect(rawbar, L::CODES + L::SCALES);
           bulk_load(raw, from + (val ? L::CODES : 0), L::CODES, rawbar);
-          bulk_load(raw_s + (i & 1) * L::SCALES, from + 2 * L::CODES + (val ? L::SCALES : 0), L::SCALES, rawbar);
+          bulk_load(raw_s + (k & 1) * L::SCALES, from + 2 * L::CODES + (val ? L::SCALES : 0), L::SCALES, rawbar);
         }
       };
       int64_t at = at_of(0);
       load(0, at);
-      for (int i = 0; i < n && ok; ++i) {
+      for (int k = 0; job0 + k * stride < UNP * n && ok; ++k) {
+        const int job = job0 + k * stride, i = job / UNP, w = job % UNP, tok = tok_a + job * 32;
         const uint32_t g = step + i, s = g & 1;
-        const int tok = tok_a + i * TOK + 32 * w;
-        const int64_t next = at_of(i + 1);
+        const int64_t next = at_of(k + 1);
         const bool here = at >= 0;
-        const uint32_t sc = raw_s + (i & 1) * L::SCALES;
+        const uint32_t sc = raw_s + (k & 1) * L::SCALES;
         // ---- the exponent of the largest scale (tokens outside the sequence do not count): scales are not negative,
         // so their bits compare as integers, infinities and NaN on top. A tile that is not there has a value
         // exponent of -inf, with which its probabilities vanish.
@@ -658,7 +657,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
-        load(i + 1, next);
+        load(k + 1, next);
         got += here;
         at = next;
       }
@@ -713,26 +712,40 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
     __syncthreads();
     ok = *abort_flag == 0;
 
-    // ---- rows to their place, by whole warps
-    for (int rr = warp; rr < tiles_q * 128; rr += WARPS) {
-      const int row = row0 + rr;
-      if (row >= n_rows) break;
+    // ---- rows to their place, four lanes to a row: block 2 jj + hi of coordinates 8 l + i is at columns
+    // 64 jj + 16 l + 2 i + hi
+    for (int rr = warp * 8 + lane / KV4_LANES; rr < tiles_q * 128; rr += WARPS * 8) {
+      const int row = row0 + rr, token = row / p.share;
       const float2 ml = r_ml[rr];
-      const float* o_row = reinterpret_cast<const float*>(smem + L::O_K) + rr * D;
-      float o[V];
+      const uint32_t o_row = smem_u32(smem) + L::O_K + rr * (D * 4);
+      float o[D / 4];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int d = lane * V + i, col = (d >> 6) * 64 + ((d & 31) >> 2) * 8 + 2 * (d & 3) + ((d >> 5) & 1);
-        o[i] = o_row[((col / 4) ^ (rr & (D / 4 - 1) & 31)) * 4 + (col & 3)];
-      }
-      const int64_t out_row = (first + row / p.share) * p.Hq + (int64_t)h * p.share + row % p.share;
+      for (int jj = 0; jj < J / 2; ++jj)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t x[4];
+          lds<4>(o_row + (((16 * jj + 4 * l + k) ^ (rr & (D / 4 - 1) & 31)) << 4), x);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) o[8 * (2 * jj + (u & 1)) + 2 * k + (u >> 1)] = __uint_as_float(x[u]);
+        }
+      const int64_t out_row = (first + token) * p.Hq + (int64_t)h * p.share + (row - token * p.share);
       if (p.splits == 1) {
-        finish_row<D>(p, o, ml.y, out_row, lane);
-      } else {
-        float* dst = p.part + (out_row * p.splits + split) * D + lane * V;
+        float scale = ml.y != 0.0f ? 1.0f / ml.y : 0.0f;  // nothing seen: zeros (a NaN sum stays)
+        if (p.c.v_rot) {
+          kv4_fwht<D / 4, KV4_LANES>(o, lane);
+          scale *= p.norm;
+        }
 #pragma unroll
-        for (int i = 0; i < V; ++i) dst[i] = o[i];
-        if (lane == 0) {
+        for (int x = 0; x < D / 4; ++x) o[x] *= scale;
+        Kv4Row<D, false> to;
+        to.from_float(o);
+        if (p.c.v_rot && p.c.v_sign) to.flip(p.c.v_sign, l);
+        if (row < n_rows) to.store(p.out, out_row * D, l);
+      } else if (row < n_rows) {
+        Kv4Row<D, true> to;
+        to.from_float(o);
+        to.store(p.part, (out_row * p.splits + split) * D, l);
+        if (l == 0) {
           p.part_ml[(out_row * p.splits + split) * 2] = ml.x;
           p.part_ml[(out_row * p.splits + split) * 2 + 1] = ml.y;
         }
