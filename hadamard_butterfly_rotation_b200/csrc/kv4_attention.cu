@@ -135,9 +135,6 @@ struct Lay {
   static constexpr int SMEM = O_BAR + W * ST * 8;
 };
 
-#ifndef KV4_MANY
-#define KV4_MANY 64
-#endif
 #ifndef KV4_HALF
 #define KV4_HALF 128
 #endif
@@ -771,10 +768,7 @@ rot_status run(const Params& p, bool q_f32, cudaStream_t s) {
 
 template <int D, int NG>
 rot_status run_rows(const Params& p, bool q_f32, int rows, cudaStream_t s) {
-  if constexpr (D < 256) {
-    if (rows > 8) return run<D, NG, 2>(p, q_f32, s);
-  }
-  return run<D, NG, 1>(p, q_f32, s);
+  return rows > 8 ? run<D, NG, 2>(p, q_f32, s) : run<D, NG, 1>(p, q_f32, s);
 }
 
 }  // namespace
@@ -783,8 +777,12 @@ Kv4Split kv4_split(int D, int B, int heads, int share, int window, int64_t max_n
   Kv4Split sp{};
   if (window > 0) max_len = std::min(max_len, max_new + window);
   const int64_t rows = max_new * share;
-  sp.many = D < 256 && rows > KV4_MANY;
-  sp.rows = sp.many ? KV4_ROWS : rows > 8 && D < 256 ? 16 : 8;
+  // The kernel for many rows costs about the same up to 128 of them; this one's time grows with every sixteen.
+  // Measured (us, this kernel / that one): D = 128, 24 x 4 key heads at 1024 tokens: 16 rows 20 / 30, 32 rows 35 / 30,
+  // 64 rows 46 / 30; 2 x 8 at 8000: 20 / 32, 36 / 32, 46 / 33. D = 64, 24 x 8 at 2000: 64 rows 62 / 79, 96 rows 85 / 82;
+  // 4 x 8 at 8000: 48 rows 46 / 45, 96 rows 67 / 46.
+  sp.many = D < 256 && rows > (D == 128 ? 24 : 64);
+  sp.rows = sp.many ? KV4_ROWS : rows > 8 ? 16 : 8;
   sp.chunks = (int)std::min<int64_t>(std::max<int64_t>((rows + sp.rows - 1) / sp.rows, 1), 1 << 20);
   if (sp.many) {
     // one CTA to an SM: the number of parts that wastes least of the last round, a CTA's start and end, and the
@@ -802,12 +800,14 @@ Kv4Split kv4_split(int D, int B, int heads, int share, int window, int64_t max_n
     }
     return sp;
   }
-  // Parts of the length: as many CTAs as fit at once, with at least four tiles to a warp; up to three times
-  // as many, which evens out uneven lengths, where a warp keeps sixteen tiles. (A CTA's own start and end
-  // cost as much as about three of a warp's tiles.)
+  // Parts of the length: as many CTAs as fit at once, with at least four tiles to a warp, or two while there is
+  // not a CTA to every SM; up to three times as many, which evens out uneven lengths, where a warp keeps sixteen
+  // tiles. (A CTA's own start and end cost as much as about three of a warp's tiles: 24 x 4 key heads of 1024 tokens
+  // took 20 us in 3 parts and 28 in 5; 4 x 2 of 5000, D = 256, 21 us in 10 parts and 18 in 20.)
   const int64_t units = std::max<int64_t>((int64_t)B * heads * sp.chunks, 1);
   const int64_t tiles = (max_len + KV4_TILE - 1) / KV4_TILE, at_once = 4 * (int64_t)sms;
-  const int64_t fit = std::min(at_once / units, (tiles + 4 * W - 1) / (4 * W));
+  const int64_t fit = std::max(std::min(at_once / units, (tiles + 4 * W - 1) / (4 * W)),
+                               std::min(sms / units, (tiles + 2 * W - 1) / (2 * W)));
   const int64_t even = std::min((3 * at_once + units - 1) / units, tiles / (16 * W));
   const int64_t want = std::max(fit, even), most = 256;
   sp.splits = (int)std::min(std::max<int64_t>(want, 1), most);

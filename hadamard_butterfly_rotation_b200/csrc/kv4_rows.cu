@@ -31,10 +31,7 @@ using namespace kv4;
 __device__ int g_kv4_rows_error = 0;
 
 constexpr int ROWS = KV4_ROWS, TOK = 128;
-#ifndef BLKN
-#define BLKN 64
-#endif
-constexpr int BLK = BLKN;  // columns of S that a softmax warp reads at a time
+constexpr int BLK = 64;  // columns of S that a softmax warp reads at a time
 constexpr int SOFT = 8, UNP = 4, VUNP = 3, WARPS = SOFT + UNP + VUNP + 1, CTA = 32 * WARPS;
 constexpr unsigned long long WAIT_NS = 1000000000ull;
 
