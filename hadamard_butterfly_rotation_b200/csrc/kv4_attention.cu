@@ -3,8 +3,11 @@
 //   o = U^T sum_t p_t v_t / sum_t p_t,   p_t = exp(scale (T q) . k_t),   k_t, v_t = code * group scale
 //
 // for every new row of every sequence, T and U the rotations that the cache stores keys and values in.
-// Bound by HBM for single tokens (the cache is read once: D + 4 D/G bytes per token and key head) and by
-// the tensor pipe and the unpacking for many rows.
+// For single tokens the floor is HBM traffic, the cache read once: D + 4 D/G bytes per token and key head. On B200
+// (64 sequences of up to 8192 tokens, 32 query heads of 128 on 8, G = 32) the kernel takes 100 us, 3.7 TB/s, 0.56 of
+// the measured copy rate: what bounds it is the latency of the unpacking's chains with four warps to a scheduler
+// (0.55 instructions per cycle and scheduler, 640 instructions per 32 tokens, HBM 43 % busy; 88 us where the lengths
+// are even). One sequence of 131000 tokens: 42 us.
 //
 // A CTA takes 8 NT query rows (row = new token x query head of one key head) and a part of the length.
 // Its warps are independent: each takes every W-th tile of 32 tokens through a ring of its own in shared
@@ -16,11 +19,13 @@
 //                  accumulator's start. One accumulator per group, scaled in fp32.
 //   P              fp32 exponentials against a reference that is only raised when a logit passes it by
 //                  2^8, binary16 towards the MMA, transposed by movmatrix, times the value scales.
-//   O^T = V^T P    value codes of two tokens paired by prmt, again as subnormals; -8 sum P from one MMA
+//   O^T = V^T P    value codes of two tokens paired by prmt, again as subnormals; -8 sum P from one more MMA
 //                  with ones per group.
+// Of the wide loads: the tile layout makes every shared-memory read of codes a conflict-free 16-byte one (kv4.cuh), and
+// a tile is one bulk copy, so that an SM has 147 KB on their way (16 warps, two tiles each).
 // Roundings below 32 bits: the rotated query (binary16 after an exact power-of-two scaling per row) and
-// P and P * scale (binary16, 2^-11 / 2 each); sums, maxima and logits are fp32. bf16 for P would round at
-// 2^-8 / 2, as coarse as the bf16 output itself.
+// P and P * scale (binary16), half a step of 2^-11 of the value each; sums, maxima and logits are fp32. bf16 for P
+// would round by 2^-8, as coarse as the bf16 output itself.
 #include <algorithm>
 #include <type_traits>
 
@@ -33,8 +38,9 @@ using namespace kv4;
 
 __device__ int g_kv4_attn_error = 0;
 
-constexpr int W = 4;              // warps of a CTA
+constexpr int W = 4;              // warps of a CTA (eight: 41 / 106 us, two: 46 / 111, for the cases above)
 constexpr int CTA = 32 * W;
+
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
@@ -49,31 +55,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 // offset nibbles u = q + 8 of two packed halves as binary16 subnormals: bits 0..3 (u 2^-24) and bits 4..7
-// (16 u 2^-24), one three-input operation each: (w & mask) ^ flip, mask and flip in registers
-struct Nibbles {
-  uint32_t lo_mask, lo_flip, hi_mask, hi_flip;
-  // Loaded from shared memory: an instruction has room for one immediate or uniform register, and a constant
-  // that the compiler knows is copied anew for every use (64 of 640 instructions per tile).
-  static __device__ __forceinline__ void store(uint32_t* to) {
-    to[0] = 0x000F000Fu;
-    to[1] = 0x00080008u;
-    to[2] = 0x00F000F0u;
-    to[3] = 0x00800080u;
-  }
-  __device__ __forceinline__ explicit Nibbles(uint32_t addr) {
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(lo_mask), "=r"(lo_flip), "=r"(hi_mask), "=r"(hi_flip) : "r"(addr));
-  }
-  __device__ __forceinline__ uint32_t lo(uint32_t w) const {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(w), "r"(lo_mask), "r"(lo_flip));
-    return d;
-  }
-  __device__ __forceinline__ uint32_t hi(uint32_t w) const {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(w), "r"(hi_mask), "r"(hi_flip));
-    return d;
-  }
-};
+// (16 u 2^-24), one three-input operation each: (w & mask) ^ flip
+// (the constants are register operands: written as (w & mask) ^ flip, both as immediates, it takes two)
+__device__ __forceinline__ uint32_t lo_nib(uint32_t w) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(w), "r"(0x000F000Fu), "r"(0x00080008u));
+  return d;
+}
+__device__ __forceinline__ uint32_t hi_nib(uint32_t w) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(w), "r"(0x00F000F0u), "r"(0x00800080u));
+  return d;
+}
 
 // Waits for a stage's copy, for at most about a second; false where it gave up
 __device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity) {
@@ -130,24 +123,21 @@ struct Lay {
   static constexpr int O_FAC = O_BIAS + BIAS;                  // per row: logit factor
   static constexpr int O_SEEN = O_FAC + ROWS * 4;              // per row: the tokens that it sees
   static constexpr int O_ML = O_SEEN + ROWS * 8;               // [W][ROWS][2]
-  static constexpr int O_NIB = O_ML + W * ROWS * 8;            // the constants of Nibbles
-  static constexpr int O_BAR = O_NIB + 16;
+  static constexpr int O_BAR = O_ML + W * ROWS * 8;
   static constexpr int SMEM = O_BAR + W * ST * 8;
 };
 
-#ifndef KV4_HALF
-#define KV4_HALF 128
-#endif
-#ifndef KV4_B128
-#define KV4_B128 4
-#endif
-constexpr int ctas_of(int D, int NT) { return NT == 1 ? (D == 64 ? 4 : D == 128 ? KV4_B128 : 2) : (D == 64 ? 3 : 2); }
+// CTAs that an SM holds, by the registers that are left to a thread (128 with four, 168 with three). Decode of 64
+// uneven sequences of up to 8192 tokens, D = 128, G = 32: 102 us with four, 106 with three; five (96 registers, spills)
+// took 165. One sequence of 131000 tokens: 43, 52 and 74 us.
+constexpr int ctas_of(int D, int NT) { return NT == 1 ? (D == 256 ? 2 : 4) : (D == 64 ? 3 : 2); }
 
 template <int D, int NG, int NT, bool QF32>
 __global__ void __launch_bounds__(CTA, ctas_of(D, NT)) attention_kernel(const __grid_constant__ Params p) {
   using L = Lay<D, NG, NT>;
   constexpr int J = D / 32, JG = J / NG, V = D / 32;
-  constexpr int HALVES = D * NT <= KV4_HALF ? 2 : 1;  // halves of a tile that are worked on together
+  // Halves of a tile that are worked on together: two while their registers fit (102 us against 107, as above)
+  constexpr int HALVES = D * NT <= 128 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::O_BAR) + warp * L::ST;
@@ -156,7 +146,6 @@ __global__ void __launch_bounds__(CTA, ctas_of(D, NT)) attention_kernel(const __
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bars + s)) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid == 0) Nibbles::store(reinterpret_cast<uint32_t*>(smem + L::O_NIB));
   __syncwarp();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -308,7 +297,6 @@ __global__ void __launch_bounds__(CTA, ctas_of(D, NT)) attention_kernel(const __
     __syncthreads();
 
     // ---- per thread: columns 2c, 2c + 1 of each n-tile
-    const Nibbles nib(smem_u32(smem + L::O_NIB));
     float fac[NT][2], ref[NT][2], sum[NT][2];
     int all_hi = high, all_lo = low;
     float o[NT][2 * J][4];
@@ -388,8 +376,8 @@ __global__ void __launch_bounds__(CTA, ctas_of(D, NT)) attention_kernel(const __
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf) {
               const uint32_t w0 = kw[hf][0][j], w1 = kw[hf][1][j], x0 = w0 >> 8, x1 = w1 >> 8;
-              const uint32_t a0[4] = {nib.lo(w0), nib.lo(w1), nib.hi(w0), nib.hi(w1)};
-              const uint32_t a1[4] = {nib.lo(x0), nib.lo(x1), nib.hi(x0), nib.hi(x1)};
+              const uint32_t a0[4] = {lo_nib(w0), lo_nib(w1), hi_nib(w0), hi_nib(w1)};
+              const uint32_t a1[4] = {lo_nib(x0), lo_nib(x1), hi_nib(x0), hi_nib(x1)};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 mma(acc[hf][nt], a0, qf[nt][0], qf[nt][1], acc[hf][nt]);
@@ -523,10 +511,10 @@ __global__ void __launch_bounds__(CTA, ctas_of(D, NT)) attention_kernel(const __
             const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
             uint32_t xa = prmt(vw[0][j / 2], vw[0][J / 2 + j / 2], sel);
             uint32_t xb = prmt(vw[1][j / 2], vw[1][J / 2 + j / 2], sel);
-            const uint32_t a0[4] = {nib.lo(xa), nib.hi(xa), nib.lo(xb), nib.hi(xb)};
+            const uint32_t a0[4] = {lo_nib(xa), hi_nib(xa), lo_nib(xb), hi_nib(xb)};
             xa >>= 8;
             xb >>= 8;
-            const uint32_t a1[4] = {nib.lo(xa), nib.hi(xa), nib.lo(xb), nib.hi(xb)};
+            const uint32_t a1[4] = {lo_nib(xa), hi_nib(xa), lo_nib(xb), hi_nib(xb)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma(o[nt][2 * j], a0, pv[nt][0], pv[nt][1], o[nt][2 * j]);

@@ -16,9 +16,14 @@
 // in the same warps a step waited for the values' stage before the next keys could be unpacked.
 // Codes become binary16 values code * scale 2^-e, e the exponent of the largest scale of the 32 tokens, so that
 // any binary16 scale stays in range: key exponents multiply the logits, value exponents the probabilities.
-// Roundings below 32 bits: query, key and value operands and P, 2^-11 / 2 relative each. The order of coordinates
-// in a row of Q and K, and of V's columns, is the one in which the unpacked words come; Q is written, and O read,
-// in the same order.
+// Roundings below 32 bits: query, key and value operands and P to binary16, half a step of 2^-11 of the value each.
+// The order of coordinates in a row of Q and K, and of V's columns, is the one in which the unpacked words come; Q is
+// written, and O read, in the same order.
+// On B200 a chunk of 2 x 1024 tokens over lengths of up to 8192 (32 query heads of 128 on 8, G = 32) takes 326 us,
+// 570 TFLOP/s, 0.35 of the measured bf16 rate. A step of 128 tokens takes about 5400 cycles, of which the 32 MMAs need
+// some 3800 (118 each: 128 columns do not reach the pipe's rate in a pipeline, and 256 do not fit in TMEM beside O); the
+// exponentials (2048 cycles of the special-function unit) and the unpacking overlap it in part (300 us without either,
+// 250 without both). 256 CTAs on 148 SMs leave the second round a third empty.
 #include <algorithm>
 
 #include "kv4_attention.cuh"
