@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import importlib
 import os
 import struct
 
@@ -489,6 +490,16 @@ def w4a4_tile_plan(M: int, N: int, K: int, G: int, sms: int, partials: bool = Fa
     return {k: int(v) for k, v in zip(keys, out)}
 
 
+torch = None  # bound when the first KV4Cache is made: an import statement in each of a call's functions costs a microsecond
+
+
+def _kv4_torch():
+    global torch, _kv4_kinds
+    if torch is None:
+        torch = importlib.import_module("torch")
+        _kv4_kinds = {torch.bfloat16: ROT_BF16, torch.float32: ROT_F32}
+
+
 class KV4Cache:
     """A paged key/value cache of one attention layer, held in 4 bits (rot_kv4_cache).
 
@@ -499,7 +510,7 @@ class KV4Cache:
     """
 
     def __init__(self, data, D: int, G: int, *, k_plan: "Plan | None" = None, v_plan: "Plan | None" = None):
-        import torch
+        _kv4_torch()
         D, G = int(D), int(G)
         if not isinstance(data, torch.Tensor) or data.dtype != torch.uint8 or data.dim() != 4:
             raise RotError(ROT_EINVAL, "data must be a 4-D uint8 tensor")
@@ -528,7 +539,7 @@ class KV4Cache:
     @classmethod
     def empty(cls, pages: int, page: int, heads: int, D: int, G: int, *, k_plan=None, v_plan=None, device="cuda"):
         """An uninitialised cache of `pages` pages of `page` tokens (a multiple of 32)."""
-        import torch
+        _kv4_torch()
         if page <= 0 or page % 32:
             raise RotError(ROT_EINVAL, f"page = {page} must be a positive multiple of 32")
         data = torch.empty((pages, heads, page // 32, cls.tile_bytes(D, G)), dtype=torch.uint8, device=device)
@@ -536,21 +547,20 @@ class KV4Cache:
 
     def _struct(self):
         """(C view, device index): checked against the current device and with the plans as they are now."""
-        import torch
         index = self.data.get_device()
         if index < 0:
             raise RotError(ROT_EINVAL, f"the cache must be on a CUDA device, not {self.data.device}")
         if index != torch.cuda.current_device():
             _check_device(index, torch.cuda.current_device(), "the cache")
         k, v = self.k_plan, self.v_plan
-        if (k is not None and not k._h.value) or (v is not None and not v._h.value):
+        kh, vh = k._h.value if k is not None else 0, v._h.value if v is not None else 0
+        if kh is None or vh is None:
             raise RotError(ROT_EINVAL, "a plan of the cache was closed")
-        return _kv4_cache_pack(*self._shape, k._h.value if k is not None else 0, v._h.value if v is not None else 0), index
+        return _kv4_cache_pack(*self._shape, kh, vh), index
 
 
 def _kv4_on(t, name: str, index: int):
     """A torch tensor on the device of that index, which is the current one (see _arg)."""
-    import torch
     if isinstance(t, torch.Tensor):
         at = t.get_device()
         if at == index:
@@ -563,28 +573,36 @@ def _kv4_on(t, name: str, index: int):
 
 def _kv4_seqs(table, lens, cu, T: int, index: int):
     """Checked rot_kv4_seqs of page table, lengths and row offsets."""
-    import torch
     i32 = torch.int32
-    _kv4_on(lens, "lens", index)
-    if lens.dim() != 1 or lens.dtype != i32 or not lens.is_contiguous():
-        raise RotError(ROT_EINVAL, "lens must be a contiguous 1-D int32 tensor")
+    try:
+        B, = lens.shape
+        rows, cols = table.shape
+        step, unit = table.stride()
+        if cu is None:
+            pc, ok = 0, T == B
+        else:
+            pc, ok = cu.data_ptr(), cu.shape == (B + 1,) and cu.dtype is i32 and cu.get_device() == index and cu.is_contiguous()
+        if (ok and rows == B and (unit == 1 or cols <= 1) and lens.dtype is i32 and table.dtype is i32
+                and lens.get_device() == index and table.get_device() == index and lens.is_contiguous()):
+            return _kv4_seqs_pack(table.data_ptr(), step if B > 1 and step > cols else cols, cols, lens.data_ptr(), pc, B, T)
+    except (AttributeError, ValueError, TypeError):
+        pass
+    # what is wrong with them
+    for t, name, dims in ((lens, "lens", 1), (table, "table", 2), (cu, "cu", 1)):
+        if t is None and name == "cu":
+            continue
+        _kv4_on(t, name, index)
+        if t.dim() != dims or t.dtype is not i32 or (dims == 1 and not t.is_contiguous()):
+            raise RotError(ROT_EINVAL, f"{name} must be a {'contiguous ' if dims == 1 else ''}{dims}-D int32 tensor, got "
+                                       f"{t.dtype} {tuple(t.shape)}")
     B = lens.shape[0]
-    _kv4_on(table, "table", index)
-    if table.dim() != 2 or table.shape[0] != B or table.dtype != i32:
-        raise RotError(ROT_EINVAL, f"table must be a 2-D int32 tensor with one row for each of {B} sequences")
-    cols = table.shape[1]
-    step, unit = table.stride()
-    if cols > 1 and unit != 1:
-        raise RotError(ROT_EINVAL, "table must have unit stride along its rows")
-    pc = 0
-    if cu is not None:
-        _kv4_on(cu, "cu", index)
-        if cu.dim() != 1 or cu.shape[0] != B + 1 or cu.dtype != i32 or not cu.is_contiguous():
-            raise RotError(ROT_EINVAL, f"cu must be a contiguous int32 tensor of {B + 1} offsets")
-        pc = cu.data_ptr()
-    elif T != B:
+    if table.shape[0] != B:
+        raise RotError(ROT_EINVAL, f"table must have one row for each of {B} sequences, got {table.shape[0]}")
+    if cu is not None and cu.shape[0] != B + 1:
+        raise RotError(ROT_EINVAL, f"cu must hold {B + 1} offsets, got {cu.shape[0]}")
+    if cu is None and T != B:
         raise RotError(ROT_EINVAL, f"without cu there is one new token per sequence: got {T} rows for {B} sequences")
-    return _kv4_seqs_pack(table.data_ptr(), step if B > 1 and step > cols else cols, cols, lens.data_ptr(), pc, B, T)
+    raise RotError(ROT_EINVAL, "table must have unit stride along its rows")
 
 
 def _kv4_rows(t, name: str, heads, D: int, index: int):
@@ -593,10 +611,9 @@ def _kv4_rows(t, name: str, heads, D: int, index: int):
     shape = t.shape
     if len(shape) != 3 or shape[2] != D or (heads is not None and shape[1] != heads):
         raise RotError(ROT_EINVAL, f"{name} must have shape [T, {'Hq' if heads is None else heads}, {D}], got {tuple(shape)}")
-    try:
-        kind = _dtype_code(t)
-    except TypeError:
-        raise RotError(ROT_EINVAL, f"{name} must be bf16 or fp32, got {t.dtype}") from None
+    kind = _kv4_kinds.get(t.dtype)
+    if kind is None:
+        raise RotError(ROT_EINVAL, f"{name} must be bf16 or fp32, got {t.dtype}")
     token, head, unit = t.stride()
     if unit != 1 and t.numel():
         raise RotError(ROT_EINVAL, f"{name} must have unit stride along its last dimension")
@@ -616,7 +633,6 @@ def _kv4_out(t, name: str, dtypes, shape, index: int):
 
 
 def _kv4_stream(stream, index: int):
-    import torch
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
@@ -624,7 +640,6 @@ def _kv4_stream(stream, index: int):
 
 def _kv4_empty(shape, dtype, device, stream):
     """torch.empty for a launch on `stream`: the memory belongs to the stream that uses it."""
-    import torch
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
@@ -650,7 +665,6 @@ def kv4_read(cache: KV4Cache, table, lens, cu=None, *, total=None, inverse: bool
     """The new tokens' keys and values as the cache holds them (cu may name whole sequences): (k, v) of
     [total, heads, D], total the packed rows (default: one for each sequence). Stored basis, or with
     inverse the original one; bf16 (default) or fp32. Rows behind the last sequence are left as they were."""
-    import torch
     cs, index = cache._struct()
     T = int(total) if total is not None else lens.shape[0]
     shape = (T, cache.heads, cache.D)
@@ -658,14 +672,15 @@ def kv4_read(cache: KV4Cache, table, lens, cu=None, *, total=None, inverse: bool
         kind = out_dtype or torch.bfloat16
         if kind is not torch.bfloat16 and kind is not torch.float32:
             raise RotError(ROT_EINVAL, f"out_dtype must be bf16 or fp32, got {kind}")
-        k, v = _kv4_empty(shape, kind, cache.data.device, stream), _kv4_empty(shape, kind, cache.data.device, stream)
+        k = _kv4_empty(shape, kind, cache.data.device, stream)
+        v = torch.empty_like(k) if stream is None else _kv4_empty(shape, kind, cache.data.device, stream)
         pk, pv = k.data_ptr(), v.data_ptr()
     else:
         k, v = out
         pk = _kv4_out(k, "out[0]", (torch.float32, torch.bfloat16), shape, index)
         pv = _kv4_out(v, "out[1]", (k.dtype,), shape, index)
     ss = _kv4_seqs(table, lens, cu, T, index)
-    _check(_lib.kv4_read(cs, ss, inverse, pk, pv, _dtype_code(k), _kv4_stream(stream, index)))
+    _check(_lib.kv4_read(cs, ss, inverse, pk, pv, _kv4_kinds[k.dtype], _kv4_stream(stream, index)))
     return k, v
 
 
@@ -693,7 +708,6 @@ def kv4_attention(q, cache: KV4Cache, table, lens, cu=None, *, max_new=None, max
     unless given; causal by position, with the last `window` tokens only if window > 0. max_new and max_len
     (the most new tokens and the longest length of a sequence) size the launch: give them where they are
     known, since they cannot be read off device tensors. workspace: uint8, allocated here if not given."""
-    import torch
     cs, index = cache._struct()
     D = cache.D
     pq, qt, qh, kind = _kv4_rows(q, "q", None, D, index)
@@ -706,7 +720,10 @@ def kv4_attention(q, cache: KV4Cache, table, lens, cu=None, *, max_new=None, max
     need = _kv4_workspace_bytes((D, cache.G, cache.heads), index, lens.shape[0], T, Hq, window, max_new, max_len)
     shape = (T, Hq, D)
     if out is None:
-        out = _kv4_empty(shape, torch.bfloat16, q.device, stream)
+        if stream is None and kind == ROT_BF16 and q.is_contiguous():
+            out = torch.empty_like(q)
+        else:
+            out = _kv4_empty(shape, torch.bfloat16, q.device, stream)
         po = out.data_ptr()
     else:
         po = _kv4_out(out, "out", (torch.bfloat16,), shape, index)

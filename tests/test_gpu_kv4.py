@@ -584,3 +584,48 @@ def test_many_rows_split_and_left_alone(lib):
     got = lib.kv4_attention(dev(q, True), sc.cache(lib), *sc.where(), max_new=800, max_len=900, causal=False)
     sc.check_attention(host(got), q, causal=False)
     lib.check_device()
+
+
+# ----------------------------------------------------------------------------- refusals of the binding
+
+def test_binding_refusals(lib):
+    """What is not of the documented type, shape, layout or device is refused before any launch."""
+    import torch
+    sc = Scene([40, 33], [2, 1], heads=2, D=64, G=32)
+    cache = sc.cache(lib)
+    table, lens, cu = sc.where()
+    q, k = dev(sc.queries(2)), dev(sc.rows(sc.k))
+    ok = dict(q=q, table=table, lens=lens, cu=cu)
+    bad = [dict(table=table.long()), dict(table=table[:1]), dict(table=table[0]), dict(table=table.t().contiguous().t()),
+           dict(table=table.cpu()), dict(table=None), dict(lens=lens.float()), dict(lens=lens[:, None]), dict(lens=lens[:1]),
+           dict(lens=lens.cpu()), dict(lens=[40, 33]), dict(cu=cu[:2]), dict(cu=cu.long()), dict(cu=cu.cpu()), dict(cu=None),
+           dict(cu=torch.zeros(6, dtype=torch.int32, device="cuda")[::2]), dict(q=q[:, :, :32]), dict(q=q[0]),
+           dict(q=q.half()), dict(q=q.cpu()), dict(q=q.transpose(1, 2).contiguous().transpose(1, 2)), dict(q=q[:, :3]),
+           dict(q=torch.zeros(3 * 4 * 64 + 1, device="cuda")[1:].view(3, 4, 64)), dict(q=None)]
+    for b in bad:
+        a = ok | b
+        with pytest.raises(lib.RotError) as e:
+            lib.kv4_attention(a["q"], cache, a["table"], a["lens"], a["cu"], max_new=2, max_len=40)
+        assert e.value.status == lib.ROT_EINVAL, b
+    for kw in (dict(out=torch.empty((3, 4, 64), device="cuda")), dict(out=torch.empty((3, 4, 65), dtype=torch.bfloat16, device="cuda")),
+               dict(max_len=1 << 20, max_new=2, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+               dict(workspace=torch.empty(16, device="cuda")), dict(window=-1), dict(window=3, causal=False),
+               dict(scale=float("nan")), dict(max_new=-1), dict(max_len=-1)):
+        with pytest.raises(lib.RotError):
+            lib.kv4_attention(q, cache, table, lens, cu, **(dict(max_new=2, max_len=40) | kw))
+    for kk, vv in ((k, k.bfloat16()), (k, k[:2]), (k[:, :1], k[:, :1]), (k.half(), k.half()), (k, None)):
+        with pytest.raises(lib.RotError):
+            lib.kv4_append(cache, kk, vv, table, lens, cu)
+    for kw in (dict(total=3, cu=None), dict(out_dtype=torch.float16), dict(out=(k, k.bfloat16())), dict(out=(k[:2], k))):
+        with pytest.raises(lib.RotError):
+            lib.kv4_read(cache, table, lens, **(dict(total=3, cu=cu) | kw))
+    sc.plan.close()
+    with pytest.raises(lib.RotError):
+        lib.kv4_attention(q, cache, table, lens, cu, max_new=2, max_len=40)
+    harp = lib.Plan(64, [4, 16], stage_params=[np.linalg.qr(np.random.default_rng(0).standard_normal((4, 4)))[0][None], None])
+    with pytest.raises(lib.RotError) as e:     # not one Walsh-Hadamard transform
+        lib.kv4_append(lib.KV4Cache(cache.data, 64, 32, k_plan=harp), k, k, table, lens, cu)
+    assert e.value.status == lib.ROT_EUNSUPPORTED
+    with pytest.raises(lib.RotError):
+        lib.KV4Cache(cache.data, 64, 32, k_plan=lib.Plan.rht(128))
+    lib.check_device()
