@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         if ((k & 31) == 0) {
           const int job = job0 + (k + lane) * stride, tok = tok_a + job * 32;
           my_at = -1;
-          if (job < UNP * n && tok < high) {
+          if (job < UNP * n && tok < high && tok + 32 > low) {  // (pages before a window may be gone)
             my_at = kv4_tile_at(p.c, b, tok >> 5, h);
             if (my_at < 0) atomicExch(&g_kv4_rows_error, (int)ROT_EINVAL);
           }

@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 
 from kv4_scene import Scene, signs_of
+from oracle import hadamard as Hd
 from oracle import kv4 as O
 
 pytestmark = pytest.mark.gpu
@@ -629,3 +630,57 @@ def test_binding_refusals(lib):
     with pytest.raises(lib.RotError):
         lib.KV4Cache(cache.data, 64, 32, k_plan=lib.Plan.rht(128))
     lib.check_device()
+
+
+@pytest.mark.parametrize("new,share", [(1, 4), (6, 2), (40, 8)])
+@pytest.mark.parametrize("n", [400, 1000])
+def test_pages_before_a_window_may_be_gone(lib, new, share, n):
+    """Table entries of pages that no row's window reaches are not looked at, by either kernel."""
+    sc = Scene([n, 333], [new, 1], heads=1, D=128, G=64, page=32)
+    cache = sc.cache(lib)
+    table, lens, cu = sc.where()
+    q = sc.queries(share)
+    w = 100
+    lib.check_device()
+    t = table.clone()
+    for b, m in ((0, new), (1, 1)):
+        t[b, :max(0, int(sc.lens[b]) - m + 1 - w) // 32] = -1
+    got = lib.kv4_attention(dev(q, True), cache, t, lens, cu, max_new=new, max_len=n, window=w)
+    sc.check_attention(host(got), q, window=w)
+    lib.check_device()
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+@pytest.mark.parametrize("which", ["keys", "values", "both apart", "no signs"])
+def test_rotations_of_keys_and_values_are_apart(lib, rows, which):
+    """Keys and values each unrotated, rotated by plans of their own, or by a plan without signs."""
+    import torch
+    D, G, n = 64, 32, 90
+    g = np.random.default_rng(len(which))
+    sk, sv = {"keys": (signs_of(D), None), "values": (None, signs_of(D)), "both apart": (signs_of(D), signs_of(D, 5)),
+              "no signs": (np.ones(D, np.int8), np.ones(D, np.int8))}[which]
+    plan = lambda s: None if s is None else lib.Plan.rht(D, None if which == "no signs" else s)
+    cache = lib.KV4Cache.empty(4, 32, 1, D, G, k_plan=plan(sk), v_plan=plan(sv))
+    k, v = (Scene.bf16(g.standard_normal((n, 1, D)) * np.where(g.random(D) < 0.1, 9.0, 1.0)) for _ in range(2))
+    i32 = lambda a: dev(np.array(a, np.int32))
+    table = i32([[2, 0, 3]])
+    lib.kv4_append(cache, dev(k), dev(v), table, i32([n]), i32([0, n]))
+    held = []
+    for x, s in ((k, sk), (v, sv)):
+        codes, scale = O.quantise_rows(x[:, 0], G, s, s is not None)
+        held.append(O.dequantise(codes, scale, G)[:, None])
+    got = lib.kv4_read(cache, table, i32([n]), i32([0, n]), total=n, out_dtype=torch.float32)
+    assert np.array_equal(host(got[0]), held[0]) and np.array_equal(host(got[1]), held[1])
+    q = Scene.bf16(g.standard_normal((rows, 1, D)))
+    turn = lambda x, s, inv: x if s is None else Hd.rht_apply(x.reshape(-1, D), s, inverse=inv).reshape(x.shape)
+    cu = [0, rows]
+    kw = dict(scale=D ** -0.5)
+    qr = turn(np.float64(q), sk, False)
+    ref = turn(O.attention(qr, [held[0]], [held[1]], [n], cu, **kw), sv, True)
+    bound = O.attention_bound(qr, [held[0]], [held[1]], [n], cu, unrotate=sv is not None, **kw)
+    out = host(lib.kv4_attention(dev(q), cache, table, i32([n]), i32(cu), max_new=rows, max_len=n))
+    assert (np.abs(out - ref) <= bound + (np.abs(ref) + bound) * 2.0 ** -8).all()
+    assert np.linalg.norm(out - ref) <= 2.0 ** -8 * np.linalg.norm(ref)
+    k_back, v_back = (host(x) for x in lib.kv4_read(cache, table, i32([n]), i32([0, n]), total=n, inverse=True, out_dtype=torch.float32))
+    for back, x, s in ((k_back, held[0], sk), (v_back, held[1], sv)):
+        assert np.abs(back - turn(x, s, True)).max() <= 9 * 2.0 ** -24 * np.abs(x).sum(-1).max()
