@@ -825,7 +825,7 @@ def check_device():
     _check(_lib.rot_check_device())
 
 
-ROT_TEST_NONE, ROT_TEST_ROTATION_COPY, ROT_TEST_W4A4_LOADS = 0, 1, 2
+ROT_TEST_NONE, ROT_TEST_ROTATION_COPY, ROT_TEST_W4A4_LOADS, ROT_TEST_KV4_LOADS = 0, 1, 2, 3
 
 
 def test_inject(fault: int, wait_ns: int = 0):

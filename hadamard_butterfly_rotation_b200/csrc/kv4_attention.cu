@@ -68,8 +68,8 @@ __device__ __forceinline__ uint32_t hi_nib(uint32_t w) {
   return d;
 }
 
-// Waits for a stage's copy, for at most about a second; false where it gave up
-__device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity) {
+// Waits for a stage's copy, for a bounded time; false where it gave up
+__device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity, unsigned long long limit) {
   uint32_t done = 0;
   unsigned long long t0 = 0;
   while (true) {
@@ -82,7 +82,7 @@ __device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity) {
     unsigned long long t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
     if (!t0) t0 = t;
-    if (t - t0 > 1000000000ull) return false;
+    if (t - t0 > limit) return false;
   }
 }
 
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(CTA, ctas_of(D, NT)) attention_kernel(const __
         return;
       }
       have |= 1u << s;
-      if (lane == 0) {
+      if (lane == 0 && !p.skip_loads) {
         const uint32_t bar = smem_u32(bars + s);
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(L::TILE) : "memory");
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -531,10 +531,10 @@ __global__ void __launch_bounds__(CTA, ctas_of(D, NT)) attention_kernel(const __
         if (i + L::ST < count) issue(i + L::ST);
         continue;
       }
-      if (!__all_sync(0xffffffffu, wait_full(smem_u32(bars + s), (phases >> s) & 1))) {
+      if (!__all_sync(0xffffffffu, wait_full(smem_u32(bars + s), (phases >> s) & 1, p.wait_ns))) {
         // the copies behind this one get the same time, then the launch's outputs are given up
         for (int t = 0; t < L::ST; ++t)
-          if (have >> t & 1) wait_full(smem_u32(bars + t), (phases >> t) & 1);
+          if (have >> t & 1) wait_full(smem_u32(bars + t), (phases >> t) & 1, p.wait_ns);
         if (lane == 0) atomicExch(&g_kv4_attn_error, (int)ROT_ETIMEOUT);
         break;
       }
@@ -819,6 +819,8 @@ rot_status kv4_attention_launch(const Kv4View& c, int D, int NG, const Kv4Query&
   p.splits = sp.splits;
   p.scale_log2 = q.scale * 1.4426950408889634f;
   p.norm = (float)(1.0 / sqrt((double)D));
+  p.wait_ns = wait_limit_ns(1000000000ull);
+  p.skip_loads = take_test_fault(TEST_FAULT_KV4_LOADS) ? 1 : 0;
   const bool f32 = q.q_dtype == ROT_F32;
   if (sp.many) {
     const rot_status st = kv4_rows_launch(p, D, NG, f32, s);

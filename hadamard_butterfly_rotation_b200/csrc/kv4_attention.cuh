@@ -22,6 +22,8 @@ struct Params {
   int Hq, share, causal, window, chunks, splits;
   float scale_log2;  // softmax scale * log2 e
   float norm;        // 1 / sqrt(D)
+  int skip_loads;    // testing hook: no cache tile is copied, so the waits for them run out
+  unsigned long long wait_ns;  // bound of every wait
 };
 
 #ifdef __CUDACC__

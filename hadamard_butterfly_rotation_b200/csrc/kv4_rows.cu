@@ -38,7 +38,6 @@ __device__ int g_kv4_rows_error = 0;
 constexpr int ROWS = KV4_ROWS, TOK = 128;
 constexpr int BLK = 64;  // columns of S that a softmax warp reads at a time
 constexpr int SOFT = 8, UNP = 4, VUNP = 3, WARPS = SOFT + UNP + VUNP + 1, CTA = 32 * WARPS;
-constexpr unsigned long long WAIT_NS = 1000000000ull;
 
 template <int D, int NG>
 struct Lay {
@@ -80,7 +79,7 @@ __device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_
 
 // Bounded wait of a converged warp for the phase of that parity; false (recorded, and told to the CTA's other
 // warps) where it gave up.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit) {
   const uint32_t addr = smem_u32(bar);
   bool ok = true;
   unsigned long long t0 = 0;
@@ -101,7 +100,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
       unsigned long long now;
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
       if (t0 == 0) t0 = now;
-      else if (now - t0 > WAIT_NS) {
+      else if (now - t0 > limit) {
         *abort_flag = 1;
         atomicExch(&g_kv4_rows_error, (int)ROT_ETIMEOUT);
         ok = false;
@@ -357,7 +356,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         for (int i = 0; i < n && ok; ++i) {
           const uint32_t g = step + i;
           const int tok = tok_a + i * TOK;
-          ok = wait(&xfull[g & 3], (g >> 2) & 1, abort_flag) && wait(&sfull[q], g & 1, abort_flag);
+          ok = wait(&xfull[g & 3], (g >> 2) & 1, abort_flag, p.wait_ns) && wait(&sfull[q], g & 1, abort_flag, p.wait_ns);
           if (!ok) break;
           tc_after();
           const bool edge = __any_sync(0xffffffffu, tok < seen.x || tok + TOK > seen.y);
@@ -372,7 +371,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
           // O, and what stands of this step's P (`done` columns of 32 bits), times factors: where a reference rises
           auto rescale = [&](float by_o, float by_p, int done) {
             if (i > 0) {  // once the MMA that adds to O is done (nothing stands there in the first step)
-              ok = wait(&odone[q], (g - 1) & 1, abort_flag);
+              ok = wait(&odone[q], (g - 1) & 1, abort_flag, p.wait_ns);
               if (!ok) return;
               tc_after();
 #pragma unroll 1
@@ -483,8 +482,8 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         }
         // ---- O to shared memory (in K's and V's place, once no MMA reads them), row by row
         if (n > 0) {
-          ok = ok && wait(&odone[q], (step + n - 1) & 1, abort_flag);
-          if (tiles_q == 2) ok = ok && wait(&odone[q ^ 1], (step + n - 1) & 1, abort_flag);
+          ok = ok && wait(&odone[q], (step + n - 1) & 1, abort_flag, p.wait_ns);
+          if (tiles_q == 2) ok = ok && wait(&odone[q ^ 1], (step + n - 1) & 1, abort_flag, p.wait_ns);
           tc_after();
         }
         r_ml[rr] = make_float2(ref, sum * (1.0f / (1 << P_SHIFT)));
@@ -537,7 +536,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         return __shfl_sync(0xffffffffu, my_at, k & 31);
       };
       auto load = [&](int k, int64_t at) {
-        if (at >= 0 && lane == 0) {
+        if (at >= 0 && lane == 0 && !p.skip_loads) {
           const uint8_t* from = p.c.data + at;
           mbar_expect(rawbar, L::CODES + L::SCALES);
           bulk_load(raw, from + (val ? L::CODES : 0), L::CODES, rawbar);
@@ -558,7 +557,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         int ex = 0;
         uint32_t odd = 0;
         if (here) {
-          ok = wait(rawbar, got & 1, abort_flag);
+          ok = wait(rawbar, got & 1, abort_flag, p.wait_ns);
           if (!ok) break;
           // the lane's token: a key's scales follow one another, a value's are the pair's, every second
           const bool in = tok + lane >= low && tok + lane < high;
@@ -599,7 +598,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         }
         // 2^-ex in both halves
         const uint32_t down = (uint32_t)__half_as_ushort(__float2half_rn(__uint_as_float((uint32_t)(127 - ex) << 23))) * 0x00010001u;
-        ok = wait(&empty[s], ((g >> 1) & 1) ^ 1, abort_flag);
+        ok = wait(&empty[s], ((g >> 1) & 1) ^ 1, abort_flag, p.wait_ns);
         if (!ok) break;
         const uint32_t to0 = smem_u32(smem) + (val ? L::O_V : L::O_K) + s * L::KV + 32 * w * 128;
         if (!here) {
@@ -667,14 +666,14 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
         unsigned long long t0, now;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
         do asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        while (now - t0 < WAIT_NS / 100);
+        while (now - t0 < 10000000ull);
       }
     } else {
       // ======================= MMA issue
       const uint32_t q_at = smem_u32(smem) + L::O_Q, k_at = smem_u32(smem) + L::O_K, v_at = smem_u32(smem) + L::O_V;
       auto pv = [&](int q, int i, bool last_q) {  // O += P V of step i
         const uint32_t g = step + i, s = g & 1;
-        ok = ok && wait(&pfull[q], g & 1, abort_flag) && wait(&vfull[s], (g >> 1) & 1, abort_flag);
+        ok = ok && wait(&pfull[q], g & 1, abort_flag, p.wait_ns) && wait(&vfull[s], (g >> 1) & 1, abort_flag, p.wait_ns);
         if (!ok) return;
         tc_after();
         const uint64_t v_desc = desc(v_at + s * L::KV, TOK * 128, 1024);
@@ -686,7 +685,7 @@ __global__ void __launch_bounds__(CTA, 1) rows_kernel(const __grid_constant__ Pa
       };
       for (int i = 0; i < n && ok; ++i) {
         const uint32_t g = step + i, s = g & 1;
-        ok = wait(&kfull[s], (g >> 1) & 1, abort_flag);
+        ok = wait(&kfull[s], (g >> 1) & 1, abort_flag, p.wait_ns);
         for (int q = 0; q < tiles_q && ok; ++q) {
           if (i > 0) pv(q, i - 1, q == tiles_q - 1);
           if (!ok) break;

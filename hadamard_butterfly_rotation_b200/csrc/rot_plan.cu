@@ -93,7 +93,7 @@ extern "C" const char* rot_last_error(void) { return g_last_error.c_str(); }
 extern "C" const char* rot_version(void) { return "rot_b200 1.1 (sm_100a)"; }
 
 extern "C" rot_status rot_test_inject(int fault, int64_t wait_ns) {
-  if (fault < TEST_FAULT_NONE || fault > TEST_FAULT_W4A4_LOADS || wait_ns < 0)
+  if (fault < TEST_FAULT_NONE || fault > TEST_FAULT_KV4_LOADS || wait_ns < 0)
     return set_error(ROT_EINVAL, "rot_test_inject: unknown fault or negative wait bound");
   g_test_wait_ns.store(wait_ns);
   g_test_fault.store(fault);

@@ -684,3 +684,25 @@ def test_rotations_of_keys_and_values_are_apart(lib, rows, which):
     k_back, v_back = (host(x) for x in lib.kv4_read(cache, table, i32([n]), i32([0, n]), total=n, inverse=True, out_dtype=torch.float32))
     for back, x, s in ((k_back, held[0], sk), (v_back, held[1], sv)):
         assert np.abs(back - turn(x, s, True)).max() <= 9 * 2.0 ** -24 * np.abs(x).sum(-1).max()
+
+
+@pytest.mark.parametrize("new", [1, 90])
+def test_bounded_waits_give_up_then_recover(lib, new):
+    """No cache tile is copied (the testing hook): the waits run out after 20 ms, the launch ends and is reported
+    once, and the next call is right. By both kernels."""
+    sc = Scene([200], [new], heads=1, D=64, G=32)
+    cache = sc.cache(lib)
+    q = sc.queries(2)
+    lib.check_device()
+    lib.test_inject(lib.ROT_TEST_KV4_LOADS, 20_000_000)
+    try:
+        lib.kv4_attention(dev(q), cache, *sc.where(), max_new=new, max_len=200)
+        with pytest.raises(lib.RotError) as e:
+            lib.check_device()
+        assert e.value.status == lib.ROT_ETIMEOUT
+    finally:
+        lib.test_inject(lib.ROT_TEST_NONE, 0)
+    lib.check_device()
+    got = lib.kv4_attention(dev(q), cache, *sc.where(), max_new=new, max_len=200)
+    sc.check_attention(host(got), q)
+    lib.check_device()
