@@ -79,15 +79,14 @@ struct Kv4Slot {
   int seq;
   int64_t pos, at;
 };
+__host__ __device__ inline Kv4Slot kv4_slot_in(const Kv4View& c, int seq, int64_t pos, int h) {
+  return {seq, pos, pos >= 0 ? kv4_tile_at(c, seq, pos >> 5, h) : -1};
+}
 __host__ __device__ inline Kv4Slot kv4_slot_of(const Kv4View& c, int64_t row, int h) {
-  Kv4Slot p{-1, -1, -1};
-  if (row >= c.T) return p;
-  p.seq = kv4_seq_of(c, row);
-  if (p.seq < 0) return p;
-  const int64_t behind = c.cu ? (int64_t)c.cu[p.seq + 1] - row : 1;  // rows from this one to its sequence's end
-  p.pos = (int64_t)c.lens[p.seq] - behind;
-  if (p.pos >= 0) p.at = kv4_tile_at(c, p.seq, p.pos >> 5, h);
-  return p;
+  const int seq = row < c.T ? kv4_seq_of(c, row) : -1;
+  if (seq < 0) return {-1, -1, -1};
+  const int64_t behind = c.cu ? (int64_t)c.cu[seq + 1] - row : 1;  // rows from this one to its sequence's end
+  return kv4_slot_in(c, seq, (int64_t)c.lens[seq] - behind, h);
 }
 
 #ifdef __CUDACC__

@@ -100,12 +100,31 @@ struct Places {
   int t[8];       // token in the tile, or -1 behind the last sequence
 };
 __device__ __forceinline__ void find(const Kv4View& c, int64_t row0, Places& places) {
-  if (threadIdx.x >= 8) return;
-  const Kv4Slot p = kv4_slot_of(c, row0 + threadIdx.x, 0);
+  if (threadIdx.x >= 32) return;
+  const int lane = threadIdx.x;
+  const int64_t row = row0 + (lane & 7);
+  Kv4Slot p{-1, -1, -1};
+  if (c.cu && c.B < 32) {
+    // All sequences at once, a lane to each, instead of a search whose steps wait for one another; of a
+    // warp, since only the lanes' sum tells the sequence
+    const int first = c.cu[lane <= c.B ? lane : c.B], len = c.lens[lane < c.B ? lane : 0];
+    int seq = -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t begun = __ballot_sync(0xffffffffu, lane <= c.B && first <= row0 + i);
+      if ((lane & 7) == i && (begun & 1) && !(begun >> c.B & 1)) seq = __popc(begun) - 1;
+    }
+    const int64_t end = __shfl_sync(0xffffffffu, first, (seq + 1) & 31);
+    const int64_t n = __shfl_sync(0xffffffffu, len, seq & 31);
+    if (seq >= 0 && row < c.T) p = kv4_slot_in(c, seq, n - (end - row), 0);
+  } else if (lane < 8) {
+    p = kv4_slot_of(c, row, 0);
+  }
+  if (lane >= 8) return;
   // a page outside the cache is an error of the call's data
   if (p.pos >= 0 && p.at < 0) atomicExch(&g_kv4_cache_error, (int)ROT_EINVAL);
-  places.at[threadIdx.x] = p.at;
-  places.t[threadIdx.x] = p.seq < 0 ? -1 : (int)(p.pos & 31);
+  places.at[lane] = p.at;
+  places.t[lane] = p.seq < 0 ? -1 : (int)(p.pos & 31);
 }
 
 // Coordinate d of T x for the row at `base`, in 64 bits, by the whole warp.
@@ -243,9 +262,18 @@ __device__ __forceinline__ void quantise(const float (&z)[D / 4], bool rot, floa
       uint32_t pair[M < 8 ? M / 2 : 4];
 #pragma unroll
       for (int i = 0; i < (M < 8 ? M : 8); i += 2) {
-        const float a = z[x + i], b = z[x + i + 1];
-        const float ta = __fmaf_rn(a, fg, magic), tb = __fmaf_rn(b, fg, magic);
-        worst = fmaxf(worst, fmaxf(fabsf(__fmaf_rn(a, fg, magic - ta)), fabsf(__fmaf_rn(b, fg, magic - tb))));
+        // t = z f + magic, and z f - (t - magic): what rounding left over
+        unsigned long long v, t, left, f2, magic2;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(z[x + i]), "f"(z[x + i + 1]));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(fg));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(magic2) : "f"(magic));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(v), "l"(f2), "l"(magic2));
+        asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(left) : "l"(magic2), "l"(t));
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(left) : "l"(v), "l"(f2), "l"(left));
+        float ta, tb, la, lb;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(ta), "=f"(tb) : "l"(t));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(la), "=f"(lb) : "l"(left));
+        worst = fmaxf(worst, fmaxf(fabsf(la), fabsf(lb)));
         pair[i / 2] = __float_as_uint(tb) * 16u + __float_as_uint(ta);
       }
       if constexpr (M >= 8) {
