@@ -195,16 +195,18 @@ struct Kv4Row {
       else v[x] = __uint_as_float(x % 2 ? w[x / 8][x % 8 / 2] & 0xffff0000u : w[x / 8][x % 8 / 2] << 16);
     }
   }
+  // Coordinates i and i + 1 of the lane's eight of block j (i even)
+  __device__ __forceinline__ void set(int j, int i, float a, float b) {
+    if constexpr (F32) {
+      w[j][i] = __float_as_uint(a);
+      w[j][i + 1] = __float_as_uint(b);
+    } else {
+      w[j][i / 2] = kv4_pack_bf16(a, b);
+    }
+  }
   __device__ __forceinline__ void from_float(const float (&v)[D / 4]) {
 #pragma unroll
-    for (int x = 0; x < D / 4; x += 2) {
-      if constexpr (F32) {
-        w[x / 8][x % 8] = __float_as_uint(v[x]);
-        w[x / 8][x % 8 + 1] = __float_as_uint(v[x + 1]);
-      } else {
-        w[x / 8][x % 8 / 2] = kv4_pack_bf16(v[x], v[x + 1]);
-      }
-    }
+    for (int x = 0; x < D / 4; x += 2) set(x / 8, x % 8, v[x], v[x + 1]);
   }
 };
 #endif

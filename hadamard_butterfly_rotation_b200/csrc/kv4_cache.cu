@@ -15,10 +15,11 @@ namespace {
 __device__ int g_kv4_cache_error = 0;
 
 constexpr int CTA = 128;  // two warps for keys, two for values
+constexpr int APPEND_ROWS = 8, READ_ROWS = 16;  // tokens of a CTA
 // CTAs that an SM holds, by the registers that are left to a thread: appending 9.2 k tokens of 8 x 128 took
 // 22 us with 4 (128 registers), 25 us with 5 and 29 us with 6, reading 65 k of them 96, 89 and 86 us.
 constexpr int append_ctas(int D) { return D == 256 ? 2 : 4; }
-constexpr int read_ctas(int D) { return D == 256 ? 2 : 6; }
+constexpr int read_ctas(int D) { return D == 256 ? 2 : 4; }
 
 // The lane's codes of token t in its tile, word j block j's eight: a key has them in one piece of D / 8 bytes,
 // a value in two of D / 16 whose halfwords are block j's lower and upper four.
@@ -88,21 +89,31 @@ struct Codes {
   }
 };
 
+__device__ __forceinline__ void scale_x2(float a, float b, float s, float& x, float& y) {
+  unsigned long long v, by;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(by) : "f"(s));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(by));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+
 // Byte offset in its tile of the scale of group g of token t
 template <int D, int NG>
 __device__ __forceinline__ int scale_at(int t, int g, bool val) {
   return val ? 32 * D + 64 * NG + ((t >> 1) * NG + g) * 4 + (t & 1) * 2 : 32 * D + (t * NG + g) * 2;
 }
 
-// The places of a CTA's eight tokens, found once for all heads.
+// The places of a CTA's R tokens (a power of two), found once for all heads.
+template <int R>
 struct Places {
-  int64_t at[8];  // byte offset of head 0's tile, or -1
-  int t[8];       // token in the tile, or -1 behind the last sequence
+  int64_t at[R];  // byte offset of head 0's tile, or -1
+  int t[R];       // token in the tile, or -1 behind the last sequence
 };
-__device__ __forceinline__ void find(const Kv4View& c, int64_t row0, Places& places) {
+template <int R>
+__device__ __forceinline__ void find(const Kv4View& c, int64_t row0, Places<R>& places) {
   if (threadIdx.x >= 32) return;
   const int lane = threadIdx.x;
-  const int64_t row = row0 + (lane & 7);
+  const int64_t row = row0 + lane % R;
   Kv4Slot p{-1, -1, -1};
   if (c.cu && c.B < 32) {
     // All sequences at once, a lane to each, instead of a search whose steps wait for one another; of a
@@ -110,17 +121,17 @@ __device__ __forceinline__ void find(const Kv4View& c, int64_t row0, Places& pla
     const int first = c.cu[lane <= c.B ? lane : c.B], len = c.lens[lane < c.B ? lane : 0];
     int seq = -1;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < R; ++i) {
       const uint32_t begun = __ballot_sync(0xffffffffu, lane <= c.B && first <= row0 + i);
-      if ((lane & 7) == i && (begun & 1) && !(begun >> c.B & 1)) seq = __popc(begun) - 1;
+      if (lane % R == i && (begun & 1) && !(begun >> c.B & 1)) seq = __popc(begun) - 1;
     }
     const int64_t end = __shfl_sync(0xffffffffu, first, (seq + 1) & 31);
     const int64_t n = __shfl_sync(0xffffffffu, len, seq & 31);
     if (seq >= 0 && row < c.T) p = kv4_slot_in(c, seq, n - (end - row), 0);
-  } else if (lane < 8) {
+  } else if (lane < R) {
     p = kv4_slot_of(c, row, 0);
   }
-  if (lane >= 8) return;
+  if (lane >= R) return;
   // a page outside the cache is an error of the call's data
   if (p.pos >= 0 && p.at < 0) atomicExch(&g_kv4_cache_error, (int)ROT_EINVAL);
   places.at[lane] = p.at;
@@ -325,10 +336,10 @@ template <int D, int NG, bool F32>
 __global__ void __launch_bounds__(CTA, append_ctas(D)) append_kernel(const __grid_constant__ Kv4View c,
                                                                          const __grid_constant__ Kv4Rows in, float norm,
                                                                          int span) {
-  __shared__ Places places;
+  __shared__ Places<APPEND_ROWS> places;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t row0 = (int64_t)blockIdx.x * 8;
+  const int64_t row0 = (int64_t)blockIdx.x * APPEND_ROWS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % KV4_LANES, i = lane / KV4_LANES;
   const int h0 = blockIdx.y * span, heads = min(span, c.heads - h0);
   const bool val = warp >= 2, rot = val ? c.v_rot : c.k_rot;
@@ -365,76 +376,138 @@ __global__ void __launch_bounds__(CTA, append_ctas(D)) append_kernel(const __gri
   }
 }
 
+// The same for sixteen tokens of which a lane holds two, i and i + 8. The transform within a block of 32
+// coordinates is a product with the matrix H of signs (-1)^popc(a & b): codes 8 + q as fp16 subnormals, exact in
+// fp32, less what the 8 adds to the block's coordinate 0. A lane's codes are its part of the A operand as they
+// lie: coordinate 8 l + 2 s + b + 4 e of the block is column 8 b + 2 l + e of step s; its sums are coordinates
+// 8 l + 2 n + e, column 2 l + e of the n-th eight. The stages over the blocks follow the scales.
 template <int D, int NG, bool F32>
 __global__ void __launch_bounds__(CTA, read_ctas(D)) read_kernel(const __grid_constant__ Kv4View c,
                                                                        const __grid_constant__ Kv4Rows out, float norm,
                                                                        int span, int inverse) {
-  __shared__ Places places;
+  constexpr int J = D / 32;
+  __shared__ Places<READ_ROWS> places;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t row0 = (int64_t)blockIdx.x * 8;
+  const int64_t row0 = (int64_t)blockIdx.x * READ_ROWS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % KV4_LANES, i = lane / KV4_LANES;
   const int h0 = blockIdx.y * span, heads = min(span, c.heads - h0);
   const bool val = warp >= 2, rot = inverse && (val ? c.v_rot : c.k_rot);
   const uint32_t* signs = val ? c.v_sign : c.k_sign;
   find(c, row0, places);
   __syncthreads();
-  const int64_t tile = places.at[i], step = (int64_t)c.tpp * c.tile_bytes;
-  const int t = places.t[i] < 0 ? 0 : places.t[i];
-  Codes<D> next;
-  uint16_t scale[NG];
+  const int64_t step = (int64_t)c.tpp * c.tile_bytes;
+  Codes<D> next[2];
+  uint16_t scale[2][NG];
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j) next.w[j] = 0;
+  for (int r = 0; r < 2; ++r) {
 #pragma unroll
-  for (int g = 0; g < NG; ++g) scale[g] = 0;
+    for (int j = 0; j < J; ++j) next[r].w[j] = 0;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) scale[r][g] = 0;
+  }
   auto fetch = [&](int h) {
-    if (tile < 0 || h >= heads) return;
-    const uint8_t* from = c.data + tile + (h0 + h) * step;
-    next.load(from, t, l, val);
+    if (h >= heads) return;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) scale[g] = *reinterpret_cast<const uint16_t*>(from + scale_at<D, NG>(t, g, val));
+    for (int r = 0; r < 2; ++r) {
+      const int64_t tile = places.at[i + 8 * r];
+      if (tile < 0) continue;
+      const int t = places.t[i + 8 * r];
+      const uint8_t* from = c.data + tile + (h0 + h) * step;
+      next[r].load(from, t, l, val);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) scale[r][g] = *reinterpret_cast<const uint16_t*>(from + scale_at<D, NG>(t, g, val));
+    }
   };
   fetch(warp & 1);
-  int64_t at = (row0 + i) * (val ? out.v_token : out.k_token) + (h0 + (warp & 1)) * (val ? out.v_head : out.k_head);
+  // this lane's part of H: rows 2 s + b + 4 e + 8 l, column 2 n + (i & 1) + 8 (i / 2); halves e
+  uint32_t H[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) H[b] = (__popc(l & i >> 1) + (b & i)) & 1 ? 0xBC00BC00u : 0x3C003C00u;
+  const float bias = l == 0 ? -256.0f * 0x1p-24f : 0.0f;
+  const int64_t tok = val ? out.v_token : out.k_token, head = val ? out.v_head : out.k_head;
+  int64_t at = (row0 + i) * tok + (h0 + (warp & 1)) * head;
+  uint8_t* base = static_cast<uint8_t*>(const_cast<void*>(val ? out.v : out.k));
 #pragma unroll 1
-  for (int h = warp & 1; h < heads; h += 2) {
-    Codes<D> codes = next;
-    codes.join(val);
-    float s[NG];
+  for (int h = warp & 1; h < heads; h += 2, at += 2 * head) {
+    Codes<D> codes[2] = {next[0], next[1]};
+    float s[2][NG];
 #pragma unroll
-    for (int g = 0; g < NG; ++g) s[g] = __half2float(__ushort_as_half(scale[g])) * (rot ? norm : 1.0f);
-    fetch(h + 2);
-    float z[D / 4];
+    for (int r = 0; r < 2; ++r) {
+      codes[r].join(val);
 #pragma unroll
-    for (int x = 0; x < D / 4; x += 2) {
-      // 2^23 + 8 + q, less 2^23 + 8: exact
-      uint32_t u[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k)  // (w & 15) ^ (2^23 + 8) in one operation
-        asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(u[k]) : "r"(codes.w[x / 8] >> (4 * ((x + k) % 8))), "r"(15u), "r"(0x4B000008u));
-      unsigned long long v, off, by;
-      asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(u[0]), "r"(u[1]));
-      asm("mov.b64 %0, {%1, %1};" : "=l"(off) : "f"(-8388616.0f));
-      asm("mov.b64 %0, {%1, %1};" : "=l"(by) : "f"(s[x / (D / 4 / NG)]));
-      asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(off));
-      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(by));
-      asm("mov.b64 {%0, %1}, %2;" : "=f"(z[x]), "=f"(z[x + 1]) : "l"(v));
+      for (int g = 0; g < NG; ++g) s[r][g] = __half2float(__ushort_as_half(scale[r][g])) * (rot ? norm * 0x1p24f : 1.0f);
     }
-    Kv4Row<D, F32> raw;
-    if (rot) kv4_fwht<D / 4, KV4_LANES>(z, lane);  // T^T = D H / sqrt(D)
-    raw.from_float(z);
-    if (rot && signs) raw.flip(signs, l);
-    if (places.t[i] >= 0) raw.store(const_cast<void*>(val ? out.v : out.k), at, l);
-    at += 2 * (val ? out.v_head : out.k_head);
+    fetch(h + 2);
+    Kv4Row<D, F32> raw[2];
+    if (rot) {
+      uint32_t a[J][2][4];
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(a[j][r][k]) : "r"(codes[r].w[j] >> (4 * k)), "r"(0x000F000Fu), "r"(0x00080008u));
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        float z[2][2 * J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          float o[4] = {n ? 0.0f : bias, 0.0f, n ? 0.0f : bias, 0.0f};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t sign = (k & n ? 0x80008000u : 0u) ^ (n & 2 ? 0x80000000u : 0u);
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                : "+f"(o[0]), "+f"(o[1]), "+f"(o[2]), "+f"(o[3])
+                : "r"(a[j][0][2 * k]), "r"(a[j][1][2 * k]), "r"(a[j][0][2 * k + 1]), "r"(a[j][1][2 * k + 1]), "r"(H[0] ^ sign),
+                  "r"(H[1] ^ sign));
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) scale_x2(o[2 * r], o[2 * r + 1], s[r][j * NG / J], z[r][2 * j], z[r][2 * j + 1]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int m = 2; m < 2 * J; m *= 2)
+#pragma unroll
+            for (int x = 0; x < 2 * J; x += 2)
+              if (!(x & m)) bfly_x2(z[r][x], z[r][x + 1], z[r][x + m], z[r][x + m + 1]);
+#pragma unroll
+          for (int j = 0; j < J; ++j) raw[r].set(j, 2 * n, z[r][2 * j], z[r][2 * j + 1]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int x = 0; x < D / 4; x += 2) {
+          // 2^23 + 8 + q, less 2^23 + 8: exact
+          float u[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {  // (w & 15) ^ (2^23 + 8) in one operation
+            uint32_t v;
+            asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(v) : "r"(codes[r].w[x / 8] >> (4 * ((x + k) % 8))), "r"(15u), "r"(0x4B000008u));
+            u[k] = __uint_as_float(v) - 8388616.0f;
+          }
+          scale_x2(u[0], u[1], s[r][x / (D / 4 / NG)], u[0], u[1]);
+          raw[r].set(x / 8, x % 8, u[0], u[1]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (rot && signs) raw[r].flip(signs, l);  // T^T = D H / sqrt(D)
+      if (places.t[i + 8 * r] >= 0) raw[r].store(base, at + 8 * r * tok, l);
+    }
   }
 }
 
 template <class K, class... A>
-rot_status launch(K kernel, const Kv4View& c, cudaStream_t s, const Kv4Rows& rows, float norm, const A&... args) {
+rot_status launch(K kernel, int rows_cta, const Kv4View& c, cudaStream_t s, const Kv4Rows& rows, float norm, const A&... args) {
   // Heads of a CTA: two (one round of its warps) while that leaves the GPU room, up to eight once there are
   // plenty of tokens, which then find their places once for all of them.
-  const int64_t groups = (c.T + 7) / 8;
-  int span = 2;
+  const int64_t groups = (c.T + rows_cta - 1) / rows_cta;
+  int span = groups * c.heads > sm_count() ? 2 : 1;
   while (span < 8 && span < c.heads && groups * ((c.heads + span - 1) / span) > 8 * (int64_t)sm_count()) span *= 2;
   const int64_t parts = (c.heads + span - 1) / span;
   if (groups > 0x7fffffff || parts > 65535) return set_error(ROT_EUNSUPPORTED, "kv4: too many rows or heads for one launch");
@@ -454,15 +527,15 @@ rot_status launch(K kernel, const Kv4View& c, cudaStream_t s, const Kv4Rows& row
 template <int D, int NG>
 rot_status run_append(const Kv4View& c, const Kv4Rows& in, cudaStream_t s) {
   const float norm = (float)(1.0 / sqrt((double)D));
-  return in.dtype == ROT_F32 ? launch(append_kernel<D, NG, true>, c, s, in, norm)
-                             : launch(append_kernel<D, NG, false>, c, s, in, norm);
+  return in.dtype == ROT_F32 ? launch(append_kernel<D, NG, true>, APPEND_ROWS, c, s, in, norm)
+                             : launch(append_kernel<D, NG, false>, APPEND_ROWS, c, s, in, norm);
 }
 
 template <int D, int NG>
 rot_status run_read(const Kv4View& c, const Kv4Rows& out, int inverse, cudaStream_t s) {
   const float norm = (float)(1.0 / sqrt((double)D));
-  return out.dtype == ROT_F32 ? launch(read_kernel<D, NG, true>, c, s, out, norm, inverse)
-                              : launch(read_kernel<D, NG, false>, c, s, out, norm, inverse);
+  return out.dtype == ROT_F32 ? launch(read_kernel<D, NG, true>, READ_ROWS, c, s, out, norm, inverse)
+                              : launch(read_kernel<D, NG, false>, READ_ROWS, c, s, out, norm, inverse);
 }
 
 }  // namespace
