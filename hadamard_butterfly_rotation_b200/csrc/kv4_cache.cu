@@ -4,9 +4,15 @@
 // 32 j + 8 l + i, i < 8, of every block j: those of piece c = l of a key in the tile layout (kv4.cuh), of the
 // pieces r = 2 l and 2 l + 1 of a value. So a lane's codes are one contiguous piece of the tile, or two, its
 // 16-bit coordinates are 16-byte pieces that the four lanes continue to 64, and no code changes lanes. The
-// Walsh-Hadamard stages over i and j run in registers, those over l are two rounds of shuffles. A warp takes
-// eight rows at a time and fetches the next eight while it works on these.
-// Both kernels are bound by HBM traffic (rows in or out at full width, codes at 4 bits).
+// Walsh-Hadamard stages over i and j run in registers, those over l are two rounds of shuffles (appending) or,
+// for exact small integers, part of a matrix product (reading). A warp fetches the next rows while it works on
+// these.
+// Rows pass HBM at full width, codes at 4 bits: 328 bytes a token, head and side of 128 bf16 coordinates in
+// groups of 32. Reading 65 k tokens of 8 x 128 takes 68 us, 5.0 TB/s, the rest being the first loads of each CTA
+// that nothing hides; with all five stages of a block by additions and shuffles it took 83 us, bound by
+// instructions. Appending 9.2 k tokens takes 22 us, 2.2 TB/s: it is bound by the instructions that take every
+// code as a 64-bit rotation would. CTAs that stay and take rows in turn, places found a turn ahead, were slower
+// (72 us and 26 us): their shares end unevenly.
 #include "kv4.cuh"
 
 namespace rotb {
@@ -17,7 +23,8 @@ __device__ int g_kv4_cache_error = 0;
 constexpr int CTA = 128;  // two warps for keys, two for values
 constexpr int APPEND_ROWS = 8, READ_ROWS = 16;  // tokens of a CTA
 // CTAs that an SM holds, by the registers that are left to a thread: appending 9.2 k tokens of 8 x 128 took
-// 22 us with 4 (128 registers), 25 us with 5 and 29 us with 6, reading 65 k of them 96, 89 and 86 us.
+// 22 us with 4 (128 registers), 25 us with 5 and 29 us with 6, reading 65 k of them 77 us with 3, 68 us with 4,
+// 88 us with 5 and 104 us with 6.
 constexpr int append_ctas(int D) { return D == 256 ? 2 : 4; }
 constexpr int read_ctas(int D) { return D == 256 ? 2 : 4; }
 
@@ -116,8 +123,8 @@ __device__ __forceinline__ void find(const Kv4View& c, int64_t row0, Places<R>& 
   const int64_t row = row0 + lane % R;
   Kv4Slot p{-1, -1, -1};
   if (c.cu && c.B < 32) {
-    // All sequences at once, a lane to each, instead of a search whose steps wait for one another; of a
-    // warp, since only the lanes' sum tells the sequence
+    // All sequences at once, a lane to each boundary, instead of a search whose steps wait for one another:
+    // 82.7 us instead of 84.2 for 65 k tokens of 6 sequences. More boundaries than lanes are searched.
     const int first = c.cu[lane <= c.B ? lane : c.B], len = c.lens[lane < c.B ? lane : 0];
     int seq = -1;
 #pragma unroll
@@ -504,8 +511,9 @@ __global__ void __launch_bounds__(CTA, read_ctas(D)) read_kernel(const __grid_co
 
 template <class K, class... A>
 rot_status launch(K kernel, int rows_cta, const Kv4View& c, cudaStream_t s, const Kv4Rows& rows, float norm, const A&... args) {
-  // Heads of a CTA: two (one round of its warps) while that leaves the GPU room, up to eight once there are
-  // plenty of tokens, which then find their places once for all of them.
+  // Heads of a CTA: one while that leaves SMs without a CTA (a thousand rows of 2 x 256 read in 3.6 us, in 5.0
+  // with two), two (one round of its warps) while it leaves the GPU room, up to eight once there are plenty of
+  // tokens, which then find their places once for all of them.
   const int64_t groups = (c.T + rows_cta - 1) / rows_cta;
   int span = groups * c.heads > sm_count() ? 2 : 1;
   while (span < 8 && span < c.heads && groups * ((c.heads + span - 1) / span) > 8 * (int64_t)sm_count()) span *= 2;

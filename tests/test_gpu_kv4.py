@@ -706,3 +706,43 @@ def test_bounded_waits_give_up_then_recover(lib, new):
     got = lib.kv4_attention(dev(q), cache, *sc.where(), max_new=new, max_len=200)
     sc.check_attention(host(got), q)
     lib.check_device()
+
+
+@pytest.mark.parametrize("B", [1, 30, 31, 32, 33, 70])
+def test_places_of_few_and_many_sequences(lib, B):
+    """Uneven and empty sequences, the first and last of them empty where there are several, before and behind the
+    number whose starts a warp looks at in one go; rows behind the last one stay."""
+    import torch
+    new = [(5 * b) % 7 * (0 < b < B - 1) if B > 1 else 19 for b in range(B)]
+    sc = Scene([n + b % 40 for b, n in enumerate(new)], new, heads=3, D=64, G=32, seed=B)
+    cache = sc.cache(lib, sc.before())
+    behind = 21
+    k, v = (torch.cat([dev(sc.rows(x)), torch.full((behind, 3, 64), float("nan"), device="cuda")]) for x in (sc.k, sc.v))
+    lib.kv4_append(cache, k, v, *sc.where())
+    assert np.array_equal(cache.data.cpu().numpy(), sc.data())
+    out = tuple(torch.full((sc.T + behind, 3, 64), -3.0, device="cuda") for _ in range(2))
+    lib.kv4_read(cache, *sc.where(), total=sc.T + behind, out=out)
+    for got, held in zip(out, (sc.keys, sc.values)):
+        assert np.array_equal(host(got[:sc.T]), sc.rows(held)) and (got[sc.T:] == -3).all()
+    lib.check_device()
+
+
+def test_a_bad_scale_reads_into_its_own_row(lib):
+    """Tokens are transformed sixteen at a time: an infinite or NaN scale reaches no other token's values."""
+    import torch
+    sc = Scene([48], [48], heads=2, D=128, G=32)
+    cache = sc.cache(lib)
+    clean = lib.kv4_read(cache, *sc.where(), total=48, inverse=True)
+    bad = [3, 11, 30]
+    x = [dev(sc.rows(r)) for r in (sc.k, sc.v)]
+    for r in x:
+        r[bad[0], :, 40] = float("nan")
+        r[bad[1], :, 7] = float("inf")
+        r[bad[2], 1] = 1e9
+    lib.kv4_append(cache, *x, *sc.where())
+    got = lib.kv4_read(cache, *sc.where(), total=48, inverse=True)
+    keep = torch.ones((48, 2), dtype=torch.bool, device="cuda")
+    keep[bad[0]], keep[bad[1]], keep[bad[2], 1] = False, False, False
+    for a, b in zip(got, clean):
+        assert torch.equal(a[keep], b[keep])
+        assert not torch.isfinite(a[~keep]).all(-1).any()
