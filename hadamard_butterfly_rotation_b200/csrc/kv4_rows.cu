@@ -19,8 +19,8 @@
 // Roundings below 32 bits: query, key and value operands and P to binary16, half a step of 2^-11 of the value each.
 // The order of coordinates in a row of Q and K, and of V's columns, is the one in which the unpacked words come; Q is
 // written, and O read, in the same order.
-// On B200 a chunk of 2 x 1024 tokens over lengths of up to 8192 (32 query heads of 128 on 8, G = 32) takes 326 us,
-// 570 TFLOP/s, 0.35 of the measured bf16 rate. A step of 128 tokens takes about 5400 cycles, of which the 32 MMAs need
+// On B200 a chunk of 2 x 1024 tokens over lengths of up to 8192 (32 query heads of 128 on 8, G = 32) takes 322 us,
+// 577 TFLOP/s, 0.35 of the measured bf16 rate. A step of 128 tokens takes about 5400 cycles, of which the 32 MMAs need
 // some 3800 (118 each: 128 columns do not reach the pipe's rate in a pipeline, and 256 do not fit in TMEM beside O); the
 // exponentials (2048 cycles of the special-function unit) and the unpacking overlap it in part (300 us without either,
 // 250 without both). 256 CTAs on 148 SMs leave the second round a third empty.
@@ -77,10 +77,9 @@ __device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_
                : "memory");
 }
 
-// Bounded wait of a converged warp for the phase of that parity; false (recorded, and told to the CTA's other
-// warps) where it gave up.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit) {
-  const uint32_t addr = smem_u32(bar);
+// The rest of a wait that did not end at once; false (recorded, and told to the CTA's other warps) where it gave
+// up. Apart from the call, since the loop's registers and code at every place cost a chunk of a prompt 5 % (338 us, not 322).
+__device__ __noinline__ bool wait_slow(uint32_t addr, uint32_t parity, volatile int* abort_flag, unsigned long long limit) {
   bool ok = true;
   unsigned long long t0 = 0;
   for (uint32_t it = 0;; ++it) {
@@ -109,6 +108,17 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     }
   }
   return __all_sync(0xffffffffu, ok);
+}
+// Bounded wait of a converged warp for the phase of that parity
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit) {
+  const uint32_t addr = smem_u32(bar);
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(addr), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, done != 0) || wait_slow(addr, parity, abort_flag, limit);
 }
 
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
